@@ -12,8 +12,8 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libsparstar.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["sparstar.cu"]
-DEPENDS = ["sparstar.cu", "ptx.cuh", "select.cuh", "attn_sm100.cuh", "mass_sm100.cuh"]
+SOURCES = ["sparstar.cu", "norm_rope.cu"]
+DEPENDS = [*SOURCES, "host.h", "ptx.cuh", "select.cuh", "attn_sm100.cuh", "mass_sm100.cuh"]
 
 
 def nvcc_path() -> str:
@@ -24,7 +24,7 @@ def nvcc_path() -> str:
 
 
 def nvcc_command(out_path: str = LIB_PATH, extra=()) -> list:
-    return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
+    return [nvcc_path(), "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17", "--threads", "0",
             "-shared", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-o", out_path,
             *[os.path.join(CSRC, s) for s in SOURCES], *extra]
 

@@ -1,5 +1,6 @@
-// Host side of the C ABI declared in include/sparstar.h, and the single translation unit
-// that instantiates every kernel of the library.
+// Host side of the C ABI declared in include/sparstar.h for the plan, the selection, the
+// attention forward pass and the analyses, and the translation unit that instantiates their
+// kernels.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -11,6 +12,7 @@
 
 #include "sparstar.h"
 #include "attn_sm100.cuh"
+#include "host.h"
 #include "mass_sm100.cuh"
 #include "select.cuh"
 
@@ -38,16 +40,8 @@ __global__ void wait_timeout_selftest_kernel(unsigned* status) {
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxCandidates = 16384;  // Top-K keys held in shared memory (64 KB)
 constexpr int64_t kMaxMapColumns = 49152;  // columns of a mapped score row (192 KB column map)
-
-struct DeviceInfo {
-  bool ready = false;
-  int major = 0, minor = 0, sms = 0;
-  unsigned* status = nullptr;
-  bool attrs_set = false;
-};
 
 std::mutex g_mutex;
 DeviceInfo g_dev[kMaxDevices];
@@ -57,6 +51,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+}  // namespace
+
 int device_info(DeviceInfo** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return SPARSTAR_ERR_CUDA;
@@ -65,6 +61,7 @@ int device_info(DeviceInfo** out) {
   if (!d.ready) {
     cudaDeviceProp prop;
     if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return SPARSTAR_ERR_CUDA;
+    d.index = dev;
     d.major = prop.major;
     d.minor = prop.minor;
     d.sms = prop.multiProcessorCount;
@@ -84,6 +81,20 @@ int device_info(DeviceInfo** out) {
   *out = &d;
   return SPARSTAR_OK;
 }
+
+int make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int d, unsigned box_rows) {
+  // 3-D view [heads][rows][d] of bf16; box = 64 elements x box_rows rows x 1 head, 128B swizzle.
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(rows) * d * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SPARSTAR_OK : SPARSTAR_ERR_CUDA;
+}
+
+namespace {
 
 int set_kernel_attrs(DeviceInfo* d) {
   std::lock_guard<std::mutex> lock(g_mutex);
@@ -126,19 +137,12 @@ int set_kernel_attrs(DeviceInfo* d) {
   return SPARSTAR_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int64_t ceil_blocks(int64_t n, int64_t block = SPARSTAR_BLOCK) { return (n + block - 1) / block; }
 bool valid_block(int block) { return block == 64 || block == 128; }
 
 // ceil(x) with a 1e-9 guard, so that a product such as 0.1875 * 16 = 3.0 stays 3.
 int64_t ceil_guarded(double x) { return static_cast<int64_t>(std::ceil(x - 1e-9)); }
 
 bool valid_segments(const sparstar_segments& s) { return s.n_text >= 0 && s.n_ctx >= 0 && s.n_cur >= 0; }
-
-size_t align256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
-
-int launch_status() { return cudaGetLastError() == cudaSuccess ? SPARSTAR_OK : SPARSTAR_ERR_CUDA; }
 
 // Workspace: [q_hi | q_lo] [k_hi | k_lo] [scores]: the block means as bf16 hi/lo pairs
 // ([H, n_blocks, d] each) and the fp32 score matrix [H, nqb, nkb].
@@ -156,25 +160,6 @@ Workspace workspace_layout(int heads, int64_t nqb, int64_t nkb, int d, bool need
   w.scores = w.k_lo + align256(kb);
   w.total = w.scores + (need_scores ? align256(static_cast<size_t>(heads) * nqb * nkb * sizeof(float)) : 0);
   return w;
-}
-
-// Launch with programmatic stream serialization: the kernel may be scheduled while the
-// previous kernel of the stream drains; it calls griddep_wait() before reading that
-// kernel's output.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                         Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Keys per lane of the warp Top-K: the smallest supported count that covers n_cand
@@ -209,19 +194,6 @@ void launch_topk(const float* S, int64_t rows, int nkb, int n_forced, int k_topk
                    static_cast<size_t>(nkb - n_forced) * 4, st, S, nkb, n_forced, k_topk, idx, cnt, kmax);
   }
 }
-
-int make_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int d, unsigned box_rows = 128) {
-  // 3-D view [heads][rows][d] of bf16; box = 64 elements x box_rows rows x 1 head, 128B swizzle.
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(rows) * d * 2};
-  cuuint32_t box[3] = {64, box_rows, 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? SPARSTAR_OK : SPARSTAR_ERR_CUDA;
-}
-
 
 }  // namespace
 }  // namespace sparstar

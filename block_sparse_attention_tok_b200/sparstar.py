@@ -6,6 +6,7 @@ binding raises if the library is missing: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -93,6 +94,26 @@ _SIGNATURES.update({
     "sparstar_read_probe": (_c.c_int, [_c.c_void_p, _c.c_size_t, _c.c_void_p, _c.c_void_p]),
     "sparstar_map_scores": (_c.c_int, [_c.c_void_p, _c.c_int, Segments, Grid, Segments, Grid, _c.c_void_p,
                                        _c.c_void_p]),
+})
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("seq_stride", ctypes.c_int64)]
+
+
+BF16 = 0
+FP32 = 1
+_X_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+_SIGNATURES.update({
+    "sparstar_qk_norm_rope": (_c.c_int, [View, View, View, _c.c_int, _c.c_int64, _c.c_int, _c.c_int, _c.c_int,
+                                         _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_float, _c.c_int,
+                                         View, View, View, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p]),
+    "sparstar_qk_norm_rope_bwd_workspace_size": (_c.c_int, [_c.c_int, _c.POINTER(_c.c_size_t)]),
+    "sparstar_qk_norm_rope_bwd": (_c.c_int, [View, View, View, View, View, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
+                                             _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_float,
+                                             _c.c_int, _c.c_int64, View, View, View, _c.c_void_p, _c.c_void_p,
+                                             _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 })
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
@@ -352,6 +373,168 @@ def read_probe(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=No
     _check(load().sparstar_read_probe(_ptr(buf), buf.numel() * buf.element_size(), _ptr(sink), _stream_ptr(stream)),
            "sparstar_read_probe")
     return sink
+
+
+# ------------------------------------------------------------------ norm, rotation, head layout
+
+@contextlib.contextmanager
+def _launch(device: torch.device, stream):
+    """Makes `device` and `stream` (None: the device's current stream) current, so that buffers
+    allocated inside belong to the stream that uses them. Yields the stream's pointer."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield int(torch.cuda.current_stream().cuda_stream) or None
+        else:
+            with torch.cuda.stream(stream):
+                yield int(stream.cuda_stream) or None
+
+
+def _check_same_device(device, **tensors):
+    if device.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+_NO_VIEW = View(None, 0, 0, 0)
+
+
+def _stride(t: torch.Tensor, dim: int) -> int:
+    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-1]
+
+
+def _view(t: Optional[torch.Tensor], token: int, head: int, seq: Optional[int] = None) -> View:
+    if t is None:
+        return _NO_VIEW
+    return View(t.data_ptr() or None, _stride(t, token), _stride(t, head), 0 if seq is None else _stride(t, seq))
+
+
+def _check_rows(name: str, t: torch.Tensor, shape, dtype, what: str):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be {what} of shape {list(shape)} with contiguous head vectors; got "
+                         f"{t.dtype} {list(t.shape)}")
+
+
+def _check_norm_rope(q, k, v, wq, wk, cos, sin):
+    """Checks of the token-major side that both directions share. Returns (N, Hq, Hk, d)."""
+    if q.dim() != 3 or q.dtype not in _X_DTYPES:
+        raise ValueError("q must be a bf16 or fp32 CUDA tensor [N, heads, d]")
+    n, hq, d = q.shape
+    if v is not None and k is None:
+        raise ValueError("v comes with k")
+    hk = k.shape[1] if k is not None and k.dim() == 3 else 0
+    for name, t, h in (("q", q, hq), ("k", k, hk), ("v", v, hk)):
+        if t is not None:
+            _check_rows(name, t, (n, h, d), q.dtype, "a tensor of q's type")
+    for name, t, shape in (("wq", wq, (d,)), ("wk", wk, (d,)), ("cos", cos, (n, d // 2)), ("sin", sin, (n, d // 2))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {list(shape)}")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    _check_same_device(q.device, q=q, k=k, v=v, wq=wq, wk=wk, cos=cos, sin=sin)
+    return n, hq, hk, d
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None,
+                 wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None,
+                 cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 kv_rows: Optional[torch.Tensor] = None, kv_offset: int = 0, stream=None):
+    """RMS norm of the queries and keys of each head, position rotation and the change to
+    head-major, in one pass. q [N, Hq, d], k and v [N, Hk, d]: bf16 or fp32, any token and head
+    strides (slices of one fused projection). wq, wk fp32 [d]; cos, sin fp32 [N, d/2]. Returns
+    (q_out, k_out, v_out), bf16; given outputs may be strided views.
+
+    q_out [Hq, N, d]. k_out and v_out [Hk, rows, d] receive token n at row kv_offset + n (default:
+    kv_offset + N rows, those before the offset unwritten), or at row kv_rows[n] (int32 [N]). With
+    kv_rows they may also be a cache [N, Hk, rows, d] that takes one token of each of N sequences.
+    A negative kv_rows[n] leaves token n out; one past the rows does too and is reported by
+    device_status()."""
+    n, hq, hk, d = _check_norm_rope(q, k, v, wq, wk, cos, sin)
+    if kv_rows is not None and (kv_rows.dtype != torch.int32 or tuple(kv_rows.shape) != (n,)
+                                or not kv_rows.is_contiguous()):
+        raise ValueError("kv_rows must be a contiguous int32 tensor [N]")
+    if kv_rows is not None and (kv_offset or (k is not None and k_out is None) or (v is not None and v_out is None)):
+        raise ValueError("kv_rows needs k_out (and v_out) and takes no kv_offset")
+    for t, o in (("k", k_out), ("v", v_out)):
+        if o is not None and (k if t == "k" else v) is None:
+            raise ValueError(f"{t}_out without {t}")
+    kv_offset = int(kv_offset)
+    if kv_offset < 0:
+        raise ValueError("kv_offset must not be negative")
+    with _launch(q.device, stream) as st:
+        bf16 = torch.bfloat16
+        if q_out is None:
+            q_out = torch.empty(hq, n, d, dtype=bf16, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(hk, kv_offset + n, d, dtype=bf16, device=q.device)
+        if v is not None and v_out is None:
+            v_out = torch.empty(hk, kv_offset + n, d, dtype=bf16, device=q.device)
+        _check_rows("q_out", q_out, (hq, n, d), bf16, "a bf16 tensor")
+        rows, dims = 0, 3
+        if k_out is not None:
+            dims, rows = k_out.dim(), k_out.shape[-2]
+            lead = (n, hk) if kv_rows is not None and dims == 4 else (hk,)
+            _check_rows("k_out", k_out, (*lead, rows, d), bf16, "a bf16 tensor")
+            if v_out is not None:
+                _check_rows("v_out", v_out, k_out.shape, bf16, "a bf16 tensor")
+        _check_same_device(q.device, q_out=q_out, k_out=k_out, v_out=v_out, kv_rows=kv_rows)
+        kv_dims = (2, 1, 0) if dims == 4 else (1, 0)
+        _check(load().sparstar_qk_norm_rope(
+            _view(q, 0, 1), _view(k, 0, 1), _view(v, 0, 1), _X_DTYPES[q.dtype], n, hq, hk, d, _ptr(wq), _ptr(wk),
+            _ptr(cos), _ptr(sin), eps, int(interleaved), _view(q_out, 1, 0), _view(k_out, *kv_dims),
+            _view(v_out, *kv_dims), _ptr(kv_rows), kv_offset, rows, st), "sparstar_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def qk_norm_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                     dv: Optional[torch.Tensor] = None, wq: Optional[torch.Tensor] = None,
+                     wk: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                     sin: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     kv_offset: int = 0, dq_in: Optional[torch.Tensor] = None, dk_in: Optional[torch.Tensor] = None,
+                     dv_in: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of qk_norm_rope (without kv_rows). dq [Hq, N, d], dk and dv [Hk, rows, d] (read at
+    rows kv_offset + n): bf16, strided views allowed. q and k are the forward call's inputs.
+    Returns (dq_in, dk_in, dv_in, dwq, dwk): token-major in q's type (given outputs may be slices
+    of one fused gradient) and fp32 [d] sums, dwq and dwk also where the weights were left out.
+    The same inputs give the same bits."""
+    n, hq, hk, d = _check_norm_rope(q, k, None, wq, wk, cos, sin)
+    if (dk is None) != (k is None) or (dv is not None and k is None):
+        raise ValueError("dk comes with k, and dv with both")
+    kv_offset = int(kv_offset)
+    _check_rows("dq", dq, (hq, n, d), torch.bfloat16, "a bf16 tensor")
+    for name, t in (("dk", dk), ("dv", dv)):
+        if t is not None:
+            rows = t.shape[1] if t.dim() == 3 else 0
+            _check_rows(name, t, (hk, rows, d), torch.bfloat16, "a bf16 tensor")
+            if kv_offset < 0 or kv_offset + n > rows:
+                raise ValueError(f"{name} has no rows {kv_offset} to {kv_offset + n}")
+    with _launch(q.device, stream) as st:
+        if dq_in is None:
+            dq_in = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
+        if dk is not None and dk_in is None:
+            dk_in = torch.empty(n, hk, d, dtype=q.dtype, device=q.device)
+        if dv is not None and dv_in is None:
+            dv_in = torch.empty(n, hk, d, dtype=q.dtype, device=q.device)
+        for name, t, src, h in (("dq_in", dq_in, dq, hq), ("dk_in", dk_in, dk, hk), ("dv_in", dv_in, dv, hk)):
+            if t is not None:
+                if src is None:
+                    raise ValueError(f"{name} without its gradient")
+                _check_rows(name, t, (n, h, d), q.dtype, "a tensor of q's type")
+        _check_same_device(q.device, dq=dq, dk=dk, dv=dv, dq_in=dq_in, dk_in=dk_in, dv_in=dv_in)
+        dw = torch.empty(2, d, dtype=torch.float32, device=q.device)
+        nbytes = ctypes.c_size_t()
+        _check(load().sparstar_qk_norm_rope_bwd_workspace_size(d, ctypes.byref(nbytes)),
+               "sparstar_qk_norm_rope_bwd_workspace_size")
+        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=q.device)
+        _check(load().sparstar_qk_norm_rope_bwd(
+            _view(dq, 1, 0), _view(dk, 1, 0), _view(dv, 1, 0), _view(q, 0, 1), _view(k, 0, 1), _X_DTYPES[q.dtype], n,
+            hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, int(interleaved), kv_offset, _view(dq_in, 0, 1),
+            _view(dk_in, 0, 1), _view(dv_in, 0, 1), _ptr(dw[0]), _ptr(dw[1]) if dk is not None else None, _ptr(ws),
+            nbytes.value, st), "sparstar_qk_norm_rope_bwd")
+    return dq_in, dk_in, dv_in, dw[0], dw[1] if dk is not None else None
 
 
 def device_status(clear: bool = True, stream=None) -> int:

@@ -265,6 +265,61 @@ int sparstar_token_bound(const void* q, const void* k, int heads, int64_t n_q, i
                          const float* lse_dense, float sm_scale, float* u_token, float* u_block,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------ norm, rotation, head layout
+ * A strided array of head vectors: the vector of (sequence s, token t, head h) starts at
+ * data + s * seq_stride + t * token_stride + h * head_stride (strides in elements), its d
+ * values contiguous. data 16-byte aligned; strides positive multiples of 16 bytes wherever
+ * the dimension is longer than one. seq_stride is 0 unless stated. */
+typedef struct sparstar_view {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int64_t seq_stride;
+} sparstar_view;
+
+#define SPARSTAR_BF16 0
+#define SPARSTAR_FP32 1
+
+/* What a layer does between its projections and the selection: RMS norm of the queries and
+ * keys of each head, position rotation, and the change from token-major to head-major, in one
+ * pass. For token n and head h, with x the projected values, w the norm weight (fp32 [d],
+ * 16-byte aligned; NULL: ones) and theta_n the token's angles (cos, sin fp32 [n_tokens, d/2];
+ * both NULL: no rotation):
+ *   u = w * x / sqrt(mean(x^2) + eps);  y = each pair (a, b) of u turned to
+ *   (a cos - b sin, b cos + a sin), pairs (i, i + d/2), or (2i, 2i + 1) if interleaved.
+ * v (data NULL in both views: none) has no norm and no rotation. q, k, v: x_dtype
+ * (SPARSTAR_BF16 or SPARSTAR_FP32); arithmetic in fp32; the outputs are bf16, rounded once.
+ * q_out: token n of head h at row n. k_out, v_out: row kv_offset + n (so that the current
+ * tokens go behind text and reference context in one [heads, Nkv, d] array), or, with kv_rows
+ * (int32 [n_tokens] device), row kv_rows[n] of sequence n when the view has a seq_stride (a
+ * cache that holds one new token of each sequence), else of the one array. A negative
+ * kv_rows[n] leaves that token's k and v unwritten (padding); one >= kv_capacity does too and
+ * records SPARSTAR_ERR_DEVICE_BOUNDS. Rows that two tokens share are left in an unspecified
+ * order of writes. Rows not named are not written.
+ * Requirements: n_tokens in [0, 2^31), heads_q >= 1, heads_k >= 0 (0: q alone), head_dim in
+ * {64, 128}, eps >= 0 and finite, kv_offset >= 0 and, without kv_rows, kv_offset + n_tokens <=
+ * kv_capacity (rows of k_out and v_out). Outputs must not overlap inputs. Requires an sm_100
+ * device. n_tokens == 0 is a no-op. */
+int sparstar_qk_norm_rope(sparstar_view q, sparstar_view k, sparstar_view v, int x_dtype, int64_t n_tokens, int heads_q,
+                          int heads_k, int head_dim, const float* wq, const float* wk, const float* cos,
+                          const float* sin, float eps, int interleaved, sparstar_view q_out, sparstar_view k_out,
+                          sparstar_view v_out, const int32_t* kv_rows, int64_t kv_offset, int64_t kv_capacity,
+                          void* stream);
+
+/* Gradient of sparstar_qk_norm_rope without kv_rows. dq, dk, dv: bf16 gradients of its outputs
+ * (dk and dv are read at rows kv_offset + n; dv data NULL with dv_in data NULL: none); q, k:
+ * its inputs. Writes dq_in, dk_in, dv_in (x_dtype, token-major) and, unless NULL, dwq, dwk
+ * (fp32 [d]: sums over tokens and heads in fp32, in a fixed order, so that the same inputs give
+ * the same bits). workspace: device, 16-byte aligned, >= the size that
+ * sparstar_qk_norm_rope_bwd_workspace_size() gives. Requirements as above; n_tokens == 0 writes
+ * zeros to dwq and dwk. */
+int sparstar_qk_norm_rope_bwd_workspace_size(int head_dim, size_t* bytes);
+int sparstar_qk_norm_rope_bwd(sparstar_view dq, sparstar_view dk, sparstar_view dv, sparstar_view q, sparstar_view k,
+                              int x_dtype, int64_t n_tokens, int heads_q, int heads_k, int head_dim, const float* wq,
+                              const float* wk, const float* cos, const float* sin, float eps, int interleaved,
+                              int64_t kv_offset, sparstar_view dq_in, sparstar_view dk_in, sparstar_view dv_in,
+                              float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronizes `stream`, then returns SPARSTAR_OK, SPARSTAR_ERR_DEVICE_TIMEOUT or
  * SPARSTAR_ERR_DEVICE_BOUNDS from the current device's status word (timeout wins), or
  * SPARSTAR_ERR_CUDA if the synchronization itself failed. clear != 0 resets the word. */
