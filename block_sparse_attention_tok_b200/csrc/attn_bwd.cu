@@ -1,0 +1,197 @@
+// Host side of sparstar_attn_bwd: argument checks, workspace layout and launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "attn_bwd_sm100.cuh"
+#include "host.h"
+
+namespace sparstar {
+namespace {
+
+std::mutex g_attr_mutex;
+bool g_attrs_set[kMaxDevices];
+
+template <int D, int B>
+int set_attrs() {
+  using C = BwdConfig<D, B>;
+  for (auto kernel : {attn_dkv_kernel<D, B>, attn_dq_kernel<D, B>}) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+      return SPARSTAR_ERR_CUDA;
+    // setmaxnreg draws on the block's launch allocation: a build with fewer registers would wait
+    // there for good, so it is refused before any launch
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return SPARSTAR_ERR_CUDA;
+    if (a.numRegs * C::kThreads < C::kRegsNeeded) return SPARSTAR_ERR_UNSUPPORTED;
+  }
+  return SPARSTAR_OK;
+}
+
+int set_kernel_attrs(const DeviceInfo* dev) {
+  std::lock_guard<std::mutex> lock(g_attr_mutex);
+  if (g_attrs_set[dev->index]) return SPARSTAR_OK;
+  int rc;
+  if ((rc = set_attrs<128, 128>()) != SPARSTAR_OK || (rc = set_attrs<64, 128>()) != SPARSTAR_OK ||
+      (rc = set_attrs<128, 64>()) != SPARSTAR_OK || (rc = set_attrs<64, 64>()) != SPARSTAR_OK)
+    return rc;
+  for (auto kernel : {reinterpret_cast<const void*>(mask_count_kernel), reinterpret_cast<const void*>(mask_fill_kernel)})
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaskMaxBlocks * 4) != cudaSuccess)
+      return SPARSTAR_ERR_CUDA;
+  g_attrs_set[dev->index] = true;
+  return SPARSTAR_OK;
+}
+
+struct BwdWorkspace {
+  size_t lse2, delta, chunk_cnt, col_at, col_row, total;
+};
+
+BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t kmax) {
+  const size_t h = static_cast<size_t>(heads);
+  const size_t rows = align256(h * nqb * block * 4);
+  BwdWorkspace w;
+  w.lse2 = 0;
+  w.delta = rows;
+  w.chunk_cnt = 2 * rows;
+  w.col_at = w.chunk_cnt + align256(h * ((nqb + kMaskRows - 1) / kMaskRows) * nkb * 4);
+  w.col_row = w.col_at + align256(h * (nkb + 1) * 4);
+  w.total = w.col_row + align256(h * nqb * kmax * 4);
+  return w;
+}
+
+// Sizes that the lists and the launch geometry hold.
+int bwd_sizes(int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, int32_t kmax) {
+  if (heads < 1 || n_q < 0 || n_kv < 1 || kmax < 1) return SPARSTAR_ERR_ARG;
+  if (head_dim != 64 && head_dim != 128) return SPARSTAR_ERR_UNSUPPORTED;
+  if (block != 64 && block != 128) return SPARSTAR_ERR_UNSUPPORTED;
+  if (n_q > INT32_MAX || n_kv > INT32_MAX || heads > 65535) return SPARSTAR_ERR_UNSUPPORTED;
+  const int64_t nqb = ceil_blocks(n_q, block), nkb = ceil_blocks(n_kv, block);
+  if (nkb > kMaskMaxBlocks || heads * nqb > INT32_MAX / 2 || heads * nkb > INT32_MAX / 2 || nqb * kmax > INT32_MAX)
+    return SPARSTAR_ERR_UNSUPPORTED;
+  return SPARSTAR_OK;
+}
+
+template <int D, int B>
+void launch_bwd(const CUtensorMap (&walk)[4], const CUtensorMap (&held)[4], BwdParams p, int heads, int sms,
+                cudaStream_t st) {
+  using C = BwdConfig<D, B>;
+  p.n_items = heads * p.nkb;
+  attn_dkv_kernel<D, B><<<p.n_items < sms ? p.n_items : sms, C::kThreads, C::kSmemBytes, st>>>(walk[0], walk[1], held[2],
+                                                                                             held[3], p);
+  p.n_items = heads * p.nqb;
+  attn_dq_kernel<D, B><<<p.n_items < sms ? p.n_items : sms, C::kThreads, C::kSmemBytes, st>>>(held[0], held[1], walk[2],
+                                                                                            walk[3], p);
+}
+
+}  // namespace
+}  // namespace sparstar
+
+using namespace sparstar;
+
+extern "C" {
+
+int sparstar_attn_bwd_workspace_size(int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, int32_t kmax,
+                                     size_t* bytes) {
+  if (bytes == nullptr) return SPARSTAR_ERR_ARG;
+  const int rc = bwd_sizes(heads, n_q, n_kv, head_dim, block, kmax);
+  if (rc != SPARSTAR_OK) return rc;
+  *bytes = bwd_layout(heads, ceil_blocks(n_q, block), ceil_blocks(n_kv, block), block, kmax).total;
+  return SPARSTAR_OK;
+}
+
+int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                      int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, const int32_t* idx,
+                      const int32_t* cnt, int32_t kmax, float sm_scale, void* dq, void* dk, void* dv, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  int rc = bwd_sizes(heads, n_q, n_kv, head_dim, block, kmax);
+  if (rc != SPARSTAR_OK) return rc;
+  if (!(sm_scale == sm_scale) || std::isinf(sm_scale)) return SPARSTAR_ERR_ARG;
+  if (dk == nullptr || dv == nullptr || !aligned16(dk) || !aligned16(dv)) return SPARSTAR_ERR_ARG;
+  if (n_q > 0) {
+    for (const void* ptr : {d_o, q, k, v, o, static_cast<const void*>(dq)})
+      if (ptr == nullptr || !aligned16(ptr)) return SPARSTAR_ERR_ARG;
+    if (lse == nullptr || idx == nullptr || cnt == nullptr || (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(idx) & 3u) != 0 || (reinterpret_cast<uintptr_t>(cnt) & 3u) != 0)
+      return SPARSTAR_ERR_ARG;
+  }
+  const int64_t nqb = ceil_blocks(n_q, block), nkb = ceil_blocks(n_kv, block);
+  const BwdWorkspace ws = bwd_layout(heads, nqb, nkb, block, kmax);
+  if (n_q > 0 && (workspace == nullptr || workspace_bytes < ws.total ||
+                  (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return SPARSTAR_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  if ((rc = device_info(&dev)) != SPARSTAR_OK) return rc;
+  if (dev->major != 10) return SPARSTAR_ERR_UNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (n_q == 0) {  // no query attends to anything: the gradients of k and v are zero
+    const size_t bytes = static_cast<size_t>(heads) * n_kv * head_dim * 2;
+    return cudaMemsetAsync(dk, 0, bytes, st) == cudaSuccess && cudaMemsetAsync(dv, 0, bytes, st) == cudaSuccess
+               ? SPARSTAR_OK
+               : SPARSTAR_ERR_CUDA;
+  }
+  if ((rc = set_kernel_attrs(dev)) != SPARSTAR_OK) return rc;
+  CUtensorMap walk[4], held[4];  // q, do, k, v: boxes of one block, and of 128 rows
+  const void* base[4] = {q, d_o, k, v};
+  for (int i = 0; i < 4; ++i) {
+    const int64_t rows = i < 2 ? n_q : n_kv;
+    if ((rc = make_map(&walk[i], base[i], rows, heads, head_dim, static_cast<unsigned>(block))) != SPARSTAR_OK ||
+        (rc = make_map(&held[i], base[i], rows, heads, head_dim)) != SPARSTAR_OK)
+      return rc;
+  }
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  float* lse2 = reinterpret_cast<float*>(w + ws.lse2);
+  float* delta = reinterpret_cast<float*>(w + ws.delta);
+  int32_t* chunk_cnt = reinterpret_cast<int32_t*>(w + ws.chunk_cnt);
+  int32_t* col_at = reinterpret_cast<int32_t*>(w + ws.col_at);
+  int32_t* col_row = reinterpret_cast<int32_t*>(w + ws.col_row);
+  BwdParams p = {};
+  p.idx = idx;
+  p.cnt = cnt;
+  p.col_row = col_row;
+  p.col_at = col_at;
+  p.lse2 = lse2;
+  p.delta = delta;
+  p.dq = static_cast<__nv_bfloat16*>(dq);
+  p.dk = static_cast<__nv_bfloat16*>(dk);
+  p.dv = static_cast<__nv_bfloat16*>(dv);
+  p.status = dev->status;
+  p.n_q = n_q;
+  p.n_kv = n_kv;
+  p.nqb = static_cast<int>(nqb);
+  p.nkb = static_cast<int>(nkb);
+  p.kmax = kmax;
+  p.scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+  p.scale_log2 = p.scale * 1.4426950408889634f;
+
+  const int64_t n_pad = nqb * block;
+  const int rows_per_cta = 256 / (head_dim / 8);
+  const dim3 rows_grid(static_cast<unsigned>((n_pad + rows_per_cta - 1) / rows_per_cta), static_cast<unsigned>(heads));
+  const auto* o16 = static_cast<const __nv_bfloat16*>(o);
+  const auto* do16 = static_cast<const __nv_bfloat16*>(d_o);
+  if (head_dim == 128)
+    bwd_rows_kernel<128><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta);
+  else
+    bwd_rows_kernel<64><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta);
+  const int n_chunks = (p.nqb + kMaskRows - 1) / kMaskRows;
+  const dim3 mask_grid(static_cast<unsigned>(n_chunks), static_cast<unsigned>(heads));
+  const size_t counters = static_cast<size_t>(nkb) * 4;
+  mask_count_kernel<<<mask_grid, 256, counters, st>>>(idx, cnt, p.nqb, p.nkb, kmax, chunk_cnt, dev->status);
+  mask_scan_kernel<<<heads, 1024, 0, st>>>(p.nkb, n_chunks, chunk_cnt, col_at);
+  mask_fill_kernel<<<mask_grid, 256, counters, st>>>(idx, cnt, p.nqb, p.nkb, kmax, chunk_cnt, col_at, col_row);
+  if (head_dim == 128) {
+    if (block == 128)
+      launch_bwd<128, 128>(walk, held, p, heads, dev->sms, st);
+    else
+      launch_bwd<128, 64>(walk, held, p, heads, dev->sms, st);
+  } else {
+    if (block == 128)
+      launch_bwd<64, 128>(walk, held, p, heads, dev->sms, st);
+    else
+      launch_bwd<64, 64>(walk, held, p, heads, dev->sms, st);
+  }
+  return launch_status();
+}
+
+}  // extern "C"

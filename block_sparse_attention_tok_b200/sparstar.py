@@ -115,6 +115,14 @@ _SIGNATURES.update({
                                              _c.c_int, _c.c_int64, View, View, View, _c.c_void_p, _c.c_void_p,
                                              _c.c_void_p, _c.c_size_t, _c.c_void_p]),
 })
+_SIGNATURES.update({
+    "sparstar_attn_bwd_workspace_size": (_c.c_int, [_c.c_int, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int, _c.c_int32,
+                                                    _c.POINTER(_c.c_size_t)]),
+    "sparstar_attn_bwd": (_c.c_int, [_c.c_void_p] * 6 + [_c.c_int, _c.c_int64, _c.c_int64, _c.c_int, _c.c_int,
+                                                         _c.c_void_p, _c.c_void_p, _c.c_int32, _c.c_float, _c.c_void_p,
+                                                         _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                                         _c.c_void_p]),
+})
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -373,6 +381,62 @@ def read_probe(buf: torch.Tensor, sink: Optional[torch.Tensor] = None, stream=No
     _check(load().sparstar_read_probe(_ptr(buf), buf.numel() * buf.element_size(), _ptr(sink), _stream_ptr(stream)),
            "sparstar_read_probe")
     return sink
+
+
+# ------------------------------------------------------------------ gradient of the attention
+
+def attn_bwd_workspace_size(heads: int, n_q: int, n_kv: int, head_dim: int, kmax: int, block: int = BLOCK) -> int:
+    out = ctypes.c_size_t()
+    _check(load().sparstar_attn_bwd_workspace_size(int(heads), int(n_q), int(n_kv), int(head_dim), int(block),
+                                                   int(kmax), ctypes.byref(out)), "sparstar_attn_bwd_workspace_size")
+    return int(out.value)
+
+
+class AttnBwdWorkspace:
+    """Reusable device workspace of attn_bwd for one shape (kmax: width of idx). Calls that may
+    overlap on the GPU need one each."""
+
+    def __init__(self, heads, n_q, n_kv, head_dim, kmax, device, block: int = BLOCK):
+        nbytes = attn_bwd_workspace_size(heads, n_q, n_kv, head_dim, kmax, block)
+        self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+        self.nbytes = nbytes
+
+
+def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+             idx: torch.Tensor, cnt: torch.Tensor, sm_scale: float = 0.0, dq: Optional[torch.Tensor] = None,
+             dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+             workspace: Optional[AttnBwdWorkspace] = None, stream=None, block: int = BLOCK):
+    """Gradient of attn over the same kept lists. do is the gradient of its output o; q, k, v, idx,
+    cnt, sm_scale and block are its arguments, o and lse its results. Returns (dq, dk, dv), bf16,
+    every element written. The same inputs give the same bits."""
+    _check_qkv(do, q, k, v, o)
+    H, n_q, d = q.shape
+    n_kv = k.shape[1]
+    nqb = -(-n_q // block) if block in (64, 128) else 0
+    if do.shape != q.shape or o.shape != q.shape or k.shape != (H, n_kv, d) or v.shape != k.shape:
+        raise ValueError("do and o must have q's shape [H, Nq, d], v k's shape [H, Nkv, d]")
+    if lse.dtype != torch.float32 or lse.shape != (H, n_q) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [H, Nq]")
+    if idx.dtype != torch.int32 or cnt.dtype != torch.int32 or not idx.is_contiguous() or not cnt.is_contiguous():
+        raise ValueError("idx/cnt must be contiguous int32")
+    if nqb and (idx.dim() != 3 or idx.shape[:2] != (H, nqb) or cnt.shape != (H, nqb)):
+        raise ValueError(f"idx must be [H, {nqb}, kmax] and cnt [H, {nqb}]")
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous bf16 {list(like.shape)}")
+    _check_same_device(q.device, do=do, k=k, v=v, o=o, lse=lse, idx=idx, cnt=cnt, dq=dq, dk=dk, dv=dv,
+                       workspace=None if workspace is None else workspace.buf)
+    kmax = max(int(idx.shape[-1]), 1)
+    with _launch(q.device, stream) as st:
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = AttnBwdWorkspace(H, n_q, n_kv, d, kmax, q.device, block)
+        _check(load().sparstar_attn_bwd(_ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), H, n_q, n_kv, d,
+                                        int(block), _ptr(idx), _ptr(cnt), kmax, float(sm_scale), _ptr(dq), _ptr(dk),
+                                        _ptr(dv), _ptr(workspace.buf), workspace.nbytes, st), "sparstar_attn_bwd")
+    return dq, dk, dv
 
 
 # ------------------------------------------------------------------ norm, rotation, head layout

@@ -204,6 +204,28 @@ int sparstar_forward_ex(const void* q, const void* k, const void* v, int heads, 
                         int32_t kmax, void* o, float* lse, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* Gradient of sparstar_attn_ex over the same kept lists. For every kept pair of a valid query
+ * token t and KV token u, with P_tu = exp(sm_scale * q_t . k_u - lse_t):
+ *   dS_tu = P_tu * (do_t . v_u - do_t . o_t),
+ *   dq_t = sm_scale * sum_u dS_tu k_u, dk_u = sm_scale * sum_t dS_tu q_t, dv_u = sum_t P_tu do_t.
+ * d_o (gradient of o), q, o, dq: bf16 [H,Nq,d]; k, v, dk, dv: bf16 [H,Nkv,d]; lse fp32 [H,Nq] and
+ * o as the forward call gave them; idx, cnt, kmax, sm_scale and block as it took them (a list in
+ * any order; a block listed twice counts twice, as there; out-of-range entries are clamped as
+ * there and SPARSTAR_ERR_DEVICE_BOUNDS is recorded). Every element of dq, dk and dv is written (dk and dv of blocks
+ * that no query block keeps: 0). Sums are fp32 in a fixed order: the same inputs give the same
+ * bits. The gradient of the selection itself is zero (a piecewise constant choice).
+ * workspace: device, 256-byte aligned, >= sparstar_attn_bwd_workspace_size() bytes; calls that
+ * may overlap on the GPU need a workspace each. Outputs must not overlap inputs.
+ * Requirements: those of sparstar_attn_ex, and ceil(n_kv / block) <= 49152, heads <= 65535 and
+ * ceil(n_q / block) * kmax <= 2^31 - 1 (else SPARSTAR_ERR_UNSUPPORTED). n_q == 0 writes zeros to dk
+ * and dv (the other pointers may then be NULL). Requires an sm_100 device. */
+int sparstar_attn_bwd_workspace_size(int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, int32_t kmax,
+                                     size_t* bytes);
+int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void* v, const void* o, const float* lse,
+                      int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, const int32_t* idx,
+                      const int32_t* cnt, int32_t kmax, float sm_scale, void* dq, void* dk, void* dv, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 /* Retained attention mass of a block mask (digest, 关键结果与论文证据, bullet 跨尺度复用损失,
  * Figure 3; block energy of eq. (5) of the CalibAtt notes): for every valid query token t,
  * R_t = exp(lse_kept[t] - lse_dense[t]), the share of its dense softmax mass on the kept
