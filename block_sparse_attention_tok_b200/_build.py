@@ -12,7 +12,7 @@ CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libsparstar.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
-SOURCES = ["sparstar.cu", "norm_rope.cu", "attn_bwd.cu"]
+SOURCES = ["sparstar.cu", "norm_rope.cu", "attn_bwd.cu", "token.cu"]
 DEPENDS = [*SOURCES, "host.h", "ptx.cuh", "select.cuh", "attn_sm100.cuh", "attn_bwd_sm100.cuh", "mass_sm100.cuh"]
 
 

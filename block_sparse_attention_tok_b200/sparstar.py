@@ -123,6 +123,17 @@ _SIGNATURES.update({
                                                          _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
                                                          _c.c_void_p]),
 })
+_TOKEN_SIZES = [_c.c_int, _c.c_int, _c.c_int, _c.c_int64, _c.c_int]
+_SIGNATURES.update({
+    "sparstar_block_means": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_int, _c.c_int, _c.c_int64, _c.c_int, _c.c_int,
+                                        _c.c_void_p, _c.c_void_p]),
+    "sparstar_token_select": (_c.c_int, [_c.c_void_p] * 3 + _TOKEN_SIZES + [_c.c_int] * 3 + [_c.c_void_p] * 3),
+    "sparstar_token_attn": (_c.c_int, [_c.c_void_p] * 4 + _TOKEN_SIZES + [_c.c_void_p, _c.c_void_p, _c.c_int,
+                                                                         _c.c_float, _c.c_void_p, _c.c_void_p,
+                                                                         _c.c_void_p]),
+    "sparstar_token_forward": (_c.c_int, [_c.c_void_p] * 5 + _TOKEN_SIZES + [_c.c_int] * 3 + [_c.c_float]
+                               + [_c.c_void_p] * 5),
+})
 NOALLOC_SCRATCH_BYTES = 128 << 20
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -599,6 +610,137 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tens
             _view(dk_in, 0, 1), _view(dv_in, 0, 1), _ptr(dw[0]), _ptr(dw[1]) if dk is not None else None, _ptr(ws),
             nbytes.value, st), "sparstar_qk_norm_rope_bwd")
     return dq_in, dk_in, dv_in, dw[0], dw[1] if dk is not None else None
+
+
+# ------------------------------------------------------------------ one query token per sequence
+
+def _check_cache(k, v, kv_len, means, q=None):
+    """Checks of a cache and what belongs to it. Returns (B, Hk, S, d)."""
+    if k.dim() != 4 or k.dtype != torch.bfloat16 or not k.is_contiguous():
+        raise ValueError("a cache must be a contiguous bf16 CUDA tensor [B, Hk, S, d]")
+    b, hk, s, d = k.shape
+    if v is not None and (v.shape != k.shape or v.dtype != k.dtype or not v.is_contiguous()):
+        raise ValueError("v must be a cache of k's shape")
+    if means is not None:
+        _check_means(means, b, hk, -(-s // BLOCK), d)
+    _check_kv_len(kv_len, b)
+    if q is not None:
+        _check_token_q(q, b, hk, d)
+    _check_same_device(k.device, k=k, v=v, kv_len=kv_len, means=means, q=q)
+    return b, hk, s, d
+
+
+def _check_means(means, b, hk, nb, d):
+    if means.dtype != torch.float32 or means.shape != (b, hk, nb, d) or not means.is_contiguous():
+        raise ValueError(f"means must be contiguous fp32 {[b, hk, nb, d]}")
+
+
+def _check_kv_len(kv_len, b):
+    if kv_len.dtype != torch.int32 or kv_len.shape != (b,) or not kv_len.is_contiguous():
+        raise ValueError("kv_len must be contiguous int32 [B]")
+
+
+def _check_token_q(q, b, hk, d):
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[0] != b or q.shape[2] != d \
+            or hk < 1 or q.shape[1] < 1 or q.shape[1] % hk:
+        raise ValueError(f"q must be contiguous bf16 [{b}, Hq, {d}] with Hq a multiple of {hk}")
+
+
+def _check_lists(idx, cnt, b, hk, keep):
+    for name, t, shape in (("idx", idx, (b, hk, keep)), ("cnt", cnt, (b, hk))):
+        if t is not None and (t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 {list(shape)}")
+
+
+def _check_token_out(o, lse, q):
+    if o is not None and (o.dtype != torch.bfloat16 or o.shape != q.shape or not o.is_contiguous()):
+        raise ValueError("o must be contiguous bf16 of q's shape")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous fp32 [B, Hq]")
+
+
+def block_means(k: torch.Tensor, kv_len: torch.Tensor, means: Optional[torch.Tensor] = None, tail_only: bool = False,
+                stream=None) -> torch.Tensor:
+    """Means of the 128-token blocks of a cache k [B, Hk, S, d] of which sequence b holds kv_len[b]
+    tokens: of every block that holds some, or (tail_only) of each sequence's last one. Writes and
+    returns means, fp32 [B, Hk, ceil(S/128), d]; blocks without tokens keep what was there (zeros
+    where means is not given)."""
+    b, hk, s, d = _check_cache(k, None, kv_len, means)
+    with _launch(k.device, stream) as st:
+        if means is None:
+            means = torch.zeros(b, hk, -(-s // BLOCK), d, dtype=torch.float32, device=k.device)
+        _check(load().sparstar_block_means(_ptr(k), _ptr(kv_len), b, hk, s, d, int(tail_only), _ptr(means), st),
+               "sparstar_block_means")
+    return means
+
+
+def token_select(q: torch.Tensor, means: torch.Tensor, kv_len: torch.Tensor, keep: int, n_sink: int = 1,
+                 n_recent: int = 1, idx: Optional[torch.Tensor] = None, cnt: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Blocks that one query token per sequence, q [B, Hq, d], keeps: per (sequence, key head) the
+    first n_sink, the last n_recent and the best others by the query heads' score against the
+    block means, `keep` in all (every block where a sequence has no more). Returns (idx int32
+    [B, Hk, keep], ascending, -1 behind the last, and cnt int32 [B, Hk])."""
+    if means.dim() != 4:
+        raise ValueError("means must be contiguous fp32 [B, Hk, blocks, d]")
+    b, hk, nb, d = means.shape
+    keep = int(keep)
+    _check_means(means, b, hk, nb, d)
+    _check_kv_len(kv_len, b)
+    _check_token_q(q, b, hk, d)
+    _check_lists(idx, cnt, b, hk, keep)
+    _check_same_device(q.device, means=means, kv_len=kv_len, idx=idx, cnt=cnt)
+    with _launch(q.device, stream) as st:
+        idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
+        cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt
+        _check(load().sparstar_token_select(_ptr(q), _ptr(means), _ptr(kv_len), b, q.shape[1], hk, nb * BLOCK, d, keep,
+                                            int(n_sink), int(n_recent), _ptr(idx), _ptr(cnt), st),
+               "sparstar_token_select")
+    return idx, cnt
+
+
+def token_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, idx: torch.Tensor,
+               cnt: torch.Tensor, sm_scale: float = 0.0, o: Optional[torch.Tensor] = None, want_lse: bool = True,
+               lse: Optional[torch.Tensor] = None, stream=None):
+    """Attention of one query token per sequence, q [B, Hq, d], over the blocks idx[..., :cnt] of the
+    cache k, v [B, Hk, S, d] that holds kv_len [B] tokens. Returns (o bf16 [B, Hq, d], lse fp32
+    [B, Hq] or None); with no kept token o is 0 and lse -inf."""
+    b, hk, s, d = _check_cache(k, v, kv_len, None, q)
+    if idx.dim() != 3:
+        raise ValueError("idx must be contiguous int32 [B, Hk, keep]")
+    _check_lists(idx, cnt, b, hk, idx.shape[2])
+    _check_token_out(o, lse, q)
+    _check_same_device(q.device, idx=idx, cnt=cnt, o=o, lse=lse)
+    with _launch(q.device, stream) as st:
+        o = torch.empty_like(q) if o is None else o
+        if want_lse and lse is None:
+            lse = torch.empty(b, q.shape[1], dtype=torch.float32, device=q.device)
+        _check(load().sparstar_token_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), b, q.shape[1], hk, s, d, _ptr(idx),
+                                          _ptr(cnt), idx.shape[2], float(sm_scale), _ptr(o), _ptr(lse), st),
+               "sparstar_token_attn")
+    return o, lse
+
+
+def token_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, means: torch.Tensor,
+                  keep: int, n_sink: int = 1, n_recent: int = 1, sm_scale: float = 0.0,
+                  o: Optional[torch.Tensor] = None, want_lse: bool = True, lse: Optional[torch.Tensor] = None,
+                  idx: Optional[torch.Tensor] = None, cnt: Optional[torch.Tensor] = None, stream=None):
+    """token_select and token_attn over its choice, in one launch. Returns (o, lse, idx, cnt)."""
+    b, hk, s, d = _check_cache(k, v, kv_len, means, q)
+    keep = int(keep)
+    _check_lists(idx, cnt, b, hk, keep)
+    _check_token_out(o, lse, q)
+    _check_same_device(q.device, idx=idx, cnt=cnt, o=o, lse=lse)
+    with _launch(q.device, stream) as st:
+        idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
+        cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt
+        o = torch.empty_like(q) if o is None else o
+        if want_lse and lse is None:
+            lse = torch.empty(b, q.shape[1], dtype=torch.float32, device=q.device)
+        _check(load().sparstar_token_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(means), b, q.shape[1], hk,
+                                             s, d, keep, int(n_sink), int(n_recent), float(sm_scale), _ptr(idx),
+                                             _ptr(cnt), _ptr(o), _ptr(lse), st), "sparstar_token_forward")
+    return o, lse, idx, cnt
 
 
 def device_status(clear: bool = True, stream=None) -> int:

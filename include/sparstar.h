@@ -342,6 +342,49 @@ int sparstar_qk_norm_rope_bwd(sparstar_view dq, sparstar_view dk, sparstar_view 
                               int64_t kv_offset, sparstar_view dq_in, sparstar_view dk_in, sparstar_view dv_in,
                               float* dwq, float* dwk, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------ one query token per sequence
+ * The selection and attention of one step of a served batch: one query token of each of n_seq
+ * sequences over its K/V cache. heads_q query heads share heads_k key heads (heads_q a multiple
+ * of heads_k, at most 16 times; query head h uses key head h / (heads_q / heads_k)).
+ *   q, o     bf16 [n_seq, heads_q, d]          lse  fp32 [n_seq, heads_q] (natural log; or NULL)
+ *   k, v     bf16 [n_seq, heads_k, capacity, d]: the cache; sequence b holds kv_len[b] tokens, whatever
+ *            lies behind them is not used, not even if it is infinite or NaN
+ *   kv_len   int32 [n_seq] device, in [0, capacity]: else clamped, and SPARSTAR_ERR_DEVICE_BOUNDS recorded
+ *   means    fp32 [n_seq, heads_k, ceil(capacity/128), d]: means of the 128-token blocks
+ *   idx      int32 [n_seq, heads_k, keep], cnt int32 [n_seq, heads_k]: kept blocks, ascending, -1 behind
+ * Limits: n_seq and heads_k <= 65535, ceil(capacity/128) <= 16384 (else SPARSTAR_ERR_UNSUPPORTED).
+ * n_seq == 0 is a no-op. No workspace. All require an sm_100 device. */
+
+/* Means of the blocks of a cache: of every block that holds tokens (tail_only == 0), or of the
+ * last one of each sequence (tail_only != 0: after a step). A partial block's mean is over the
+ * tokens it holds. Means of blocks without tokens are not written. */
+int sparstar_block_means(const void* k, const int32_t* kv_len, int n_seq, int heads_k, int64_t capacity, int head_dim,
+                         int tail_only, float* means, void* stream);
+
+/* Chooses the blocks of each (sequence, key head). A sequence of at most `keep` blocks keeps them
+ * all (cnt < keep where it has fewer); a longer one keeps its first n_sink and last n_recent blocks and, of the rest,
+ * those with the largest score (sum of the sharing query heads' q) . mean, up to `keep` in all:
+ * exact ranks of fp64 scores, equal scores to the lower block, NaN below every number, -0 = +0.
+ * The means of the forced blocks are not read, so the last, partial block's need not be kept up.
+ * Requirements: keep >= 1, n_sink >= 0, n_recent >= 1, n_sink + n_recent <= keep. */
+int sparstar_token_select(const void* q, const float* means, const int32_t* kv_len, int n_seq, int heads_q, int heads_k,
+                          int64_t capacity, int head_dim, int keep, int n_sink, int n_recent, int32_t* idx,
+                          int32_t* cnt, void* stream);
+
+/* Attention of each query head over the tokens of the blocks idx[..][0..cnt-1] (any order; a block
+ * listed twice counts twice): o = softmax(sm_scale q . k) v, sm_scale <= 0 selects 1/sqrt(d).
+ * With no kept token o = 0 and lse = -inf. An entry that names no block with tokens is skipped,
+ * a cnt outside [0, keep] is clamped; both record SPARSTAR_ERR_DEVICE_BOUNDS. */
+int sparstar_token_attn(const void* q, const void* k, const void* v, const int32_t* kv_len, int n_seq, int heads_q,
+                        int heads_k, int64_t capacity, int head_dim, const int32_t* idx, const int32_t* cnt, int keep,
+                        float sm_scale, void* o, float* lse, void* stream);
+
+/* sparstar_token_select and sparstar_token_attn over its choice, in one launch. */
+int sparstar_token_forward(const void* q, const void* k, const void* v, const int32_t* kv_len, const float* means,
+                           int n_seq, int heads_q, int heads_k, int64_t capacity, int head_dim, int keep, int n_sink,
+                           int n_recent, float sm_scale, int32_t* idx, int32_t* cnt, void* o, float* lse,
+                           void* stream);
+
 /* Synchronizes `stream`, then returns SPARSTAR_OK, SPARSTAR_ERR_DEVICE_TIMEOUT or
  * SPARSTAR_ERR_DEVICE_BOUNDS from the current device's status word (timeout wins), or
  * SPARSTAR_ERR_CUDA if the synchronization itself failed. clear != 0 resets the word. */
