@@ -18,16 +18,14 @@ bool g_attrs_set[kMaxDevices];
 template <int D, int B>
 int set_attrs() {
   using C = BwdConfig<D, B>;
-  for (auto kernel : {attn_dkv_kernel<D, B>, attn_dq_kernel<D, B>}) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
-      return SPARSTAR_ERR_CUDA;
-    // setmaxnreg draws on the block's launch allocation: a build with fewer registers would wait
-    // there for good, so it is refused before any launch
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return SPARSTAR_ERR_CUDA;
-    if (a.numRegs * C::kThreads < C::kRegsNeeded) return SPARSTAR_ERR_UNSUPPORTED;
-  }
-  return SPARSTAR_OK;
+  auto* kernel = attn_bwd_kernel<D, B>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
+    return SPARSTAR_ERR_CUDA;
+  // setmaxnreg draws on the block's launch allocation: a build with fewer registers would wait
+  // there for good, so it is refused before any launch
+  cudaFuncAttributes a;
+  if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return SPARSTAR_ERR_CUDA;
+  return a.numRegs * C::kThreads < C::kRegsNeeded ? SPARSTAR_ERR_UNSUPPORTED : SPARSTAR_OK;
 }
 
 int set_kernel_attrs(const DeviceInfo* dev) {
@@ -45,16 +43,17 @@ int set_kernel_attrs(const DeviceInfo* dev) {
 }
 
 struct BwdWorkspace {
-  size_t lse2, delta, chunk_cnt, col_at, col_row, total;
+  size_t next, lse2, delta, chunk_cnt, col_at, col_row, total;
 };
 
 BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t kmax) {
   const size_t h = static_cast<size_t>(heads);
   const size_t rows = align256(h * nqb * block * 4);
   BwdWorkspace w;
-  w.lse2 = 0;
-  w.delta = rows;
-  w.chunk_cnt = 2 * rows;
+  w.next = 0;
+  w.lse2 = 256;
+  w.delta = w.lse2 + rows;
+  w.chunk_cnt = w.delta + rows;
   w.col_at = w.chunk_cnt + align256(h * ((nqb + kMaskRows - 1) / kMaskRows) * nkb * 4);
   w.col_row = w.col_at + align256(h * (nkb + 1) * 4);
   w.total = w.col_row + align256(h * nqb * kmax * 4);
@@ -74,15 +73,10 @@ int bwd_sizes(int heads, int64_t n_q, int64_t n_kv, int head_dim, int block, int
 }
 
 template <int D, int B>
-void launch_bwd(const CUtensorMap (&walk)[4], const CUtensorMap (&held)[4], BwdParams p, int heads, int sms,
-                cudaStream_t st) {
+void launch_bwd(const BwdMaps& maps, const BwdParams& p, int sms, cudaStream_t st) {
   using C = BwdConfig<D, B>;
-  p.n_items = heads * p.nkb;
-  attn_dkv_kernel<D, B><<<p.n_items < sms ? p.n_items : sms, C::kThreads, C::kSmemBytes, st>>>(walk[0], walk[1], held[2],
-                                                                                             held[3], p);
-  p.n_items = heads * p.nqb;
-  attn_dq_kernel<D, B><<<p.n_items < sms ? p.n_items : sms, C::kThreads, C::kSmemBytes, st>>>(held[0], held[1], walk[2],
-                                                                                            walk[3], p);
+  const int items = p.n_dkv + p.n_dq;
+  attn_bwd_kernel<D, B><<<items < sms ? items : sms, C::kThreads, C::kSmemBytes, st>>>(maps, p);
 }
 
 }  // namespace
@@ -132,12 +126,12 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
                : SPARSTAR_ERR_CUDA;
   }
   if ((rc = set_kernel_attrs(dev)) != SPARSTAR_OK) return rc;
-  CUtensorMap walk[4], held[4];  // q, do, k, v: boxes of one block, and of 128 rows
+  BwdMaps maps;
   const void* base[4] = {q, d_o, k, v};
   for (int i = 0; i < 4; ++i) {
     const int64_t rows = i < 2 ? n_q : n_kv;
-    if ((rc = make_map(&walk[i], base[i], rows, heads, head_dim, static_cast<unsigned>(block))) != SPARSTAR_OK ||
-        (rc = make_map(&held[i], base[i], rows, heads, head_dim)) != SPARSTAR_OK)
+    if ((rc = make_map(&maps.walk[i], base[i], rows, heads, head_dim, static_cast<unsigned>(block))) != SPARSTAR_OK ||
+        (rc = make_map(&maps.held[i], base[i], rows, heads, head_dim)) != SPARSTAR_OK)
       return rc;
   }
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -157,11 +151,14 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.status = dev->status;
+  p.next = reinterpret_cast<int*>(w + ws.next);
   p.n_q = n_q;
   p.n_kv = n_kv;
   p.nqb = static_cast<int>(nqb);
   p.nkb = static_cast<int>(nkb);
   p.kmax = kmax;
+  p.n_dkv = static_cast<int>(heads * nkb);
+  p.n_dq = static_cast<int>(heads * nqb);
   p.scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   p.scale_log2 = p.scale * 1.4426950408889634f;
 
@@ -171,9 +168,9 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   const auto* o16 = static_cast<const __nv_bfloat16*>(o);
   const auto* do16 = static_cast<const __nv_bfloat16*>(d_o);
   if (head_dim == 128)
-    bwd_rows_kernel<128><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta);
+    bwd_rows_kernel<128><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta, p.next);
   else
-    bwd_rows_kernel<64><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta);
+    bwd_rows_kernel<64><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta, p.next);
   const int n_chunks = (p.nqb + kMaskRows - 1) / kMaskRows;
   const dim3 mask_grid(static_cast<unsigned>(n_chunks), static_cast<unsigned>(heads));
   const size_t counters = static_cast<size_t>(nkb) * 4;
@@ -182,14 +179,14 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   mask_fill_kernel<<<mask_grid, 256, counters, st>>>(idx, cnt, p.nqb, p.nkb, kmax, chunk_cnt, col_at, col_row);
   if (head_dim == 128) {
     if (block == 128)
-      launch_bwd<128, 128>(walk, held, p, heads, dev->sms, st);
+      launch_bwd<128, 128>(maps, p, dev->sms, st);
     else
-      launch_bwd<128, 64>(walk, held, p, heads, dev->sms, st);
+      launch_bwd<128, 64>(maps, p, dev->sms, st);
   } else {
     if (block == 128)
-      launch_bwd<64, 128>(walk, held, p, heads, dev->sms, st);
+      launch_bwd<64, 128>(maps, p, dev->sms, st);
     else
-      launch_bwd<64, 64>(walk, held, p, heads, dev->sms, st);
+      launch_bwd<64, 64>(maps, p, dev->sms, st);
   }
   return launch_status();
 }

@@ -6,16 +6,16 @@
 //   dq_t = s sum_u dS_tu k_u.
 // P is recomputed from lse, so nothing of the forward pass's tiles is kept.
 //
-// Two passes over the kept tiles instead of one with an atomic sum: dkv_kernel holds a KV block
-// and walks the query blocks that keep it (4 products a tile), dq_kernel holds a query block
+// Two passes over the kept tiles instead of one with an atomic sum: a dK/dV item holds a KV block
+// and walks the query blocks that keep it (4 products a tile), a dQ item holds a query block
 // and walks its KV blocks (3 products a tile). That is 7 products where 5 would do, but every
 // output element has one writer and a fixed order of additions, so the same inputs give the
 // same bits, as in the forward pass; the one-pass form would also add 64 KB of fp32 reductions
 // a tile (about twice what the tile reads) and has no room for them in tensor memory.
 //
-// Both kernels: persistent, one CTA per SM, 8 softmax warps (two per TMEM lane quarter, each
-// pair splitting the 128 columns of a tile), a TMA warp, an MMA warp. A thread keeps half a row
-// of P in fp32 registers between the two halves of its work (P from S, dS from dP).
+// One persistent kernel does both, one CTA per SM: 8 softmax warps (two per TMEM lane quarter,
+// each pair splitting the 128 columns of a tile), a TMA warp, an MMA warp. A thread keeps half a
+// row of P in fp32 registers between the two halves of its work (P from S, dS from dP).
 // P and dS are rounded to bf16 as operands of the tensor cores (half a step, 2^-9 of the value
 // on average, as the forward pass rounds P); all sums are fp32.
 #pragma once
@@ -66,8 +66,10 @@ struct BwdParams {
   const float* delta;      // [H, nqb * B], 0 past n_q
   __nv_bfloat16 *dq, *dk, *dv;
   unsigned* status;
+  int* next;               // item counter, 0 at launch
   int64_t n_q, n_kv;
-  int nqb, nkb, kmax, n_items;
+  int nqb, nkb, kmax;
+  int n_dkv, n_dq;         // items of either kind
   float scale, scale_log2;
 };
 
@@ -81,41 +83,61 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// Barriers of both kernels (dkv names in comments; dq: A = K, B = V, held = Q and dO).
+// Tensor maps of q, do, k, v: boxes of one block (walked), and of 128 rows (held).
+struct BwdMaps {
+  CUtensorMap walk[4], held[4];
+};
+
+// Barriers of one kind of items (dK/dV names in comments; dQ: a = K, b = V, held = Q and dO).
+struct BwdPhaseBars {
+  uint64_t a_full[3], a_empty[3];    // walked operand of two products (Q)
+  uint64_t b_full[2], b_empty[2];    // the other walked operand (dO)
+  uint64_t st_full[2], st_empty[2];  // lse and delta of the walked rows (dK/dV only)
+  uint64_t held_full, held_empty;    // the held pair of tiles (K, V)
+  uint64_t s_full[2], p_full;        // S ready / P written
+  uint64_t dp_full, dp_read;         // dP ready / dP taken into registers (dQ only)
+  uint64_t ds_full, acc_full;
+};
+
 struct BwdBars {
-  uint64_t a_full[3], a_empty[3];   // walked operand of two products (Q)
-  uint64_t b_full[2], b_empty[2];   // the other walked operand (dO)
-  uint64_t st_full[2], st_empty[2]; // lse and delta of the walked rows (dkv only)
-  uint64_t held_full, held_empty;   // the held pair of tiles (K, V)
-  uint64_t s_full[2], p_full;       // S ready / P written
-  uint64_t dp_full, dp_read;        // dP ready / dP taken into registers (dq only)
-  uint64_t ds_full, acc_full, drain;
+  BwdPhaseBars dkv, dq;
+  uint64_t item_full[2], item_empty[2];
+  uint64_t smem_free, tmem_free, drain;
+  int32_t item[2], n_ent[2];
   uint32_t tmem;
   uint32_t abort_flag;
 };
 static_assert(sizeof(BwdBars) <= 1024, "barrier block");
 
-__device__ __forceinline__ void bwd_bars_init(BwdBars* b) {
-  for (int i = 0; i < 3; ++i) {
-    mbar_init(&b->a_full[i], 1);
-    mbar_init(&b->a_empty[i], 1);
+__device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
+  for (BwdPhaseBars* b : {&bars->dkv, &bars->dq}) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&b->a_full[i], 1);
+      mbar_init(&b->a_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b->b_full[i], 1);
+      mbar_init(&b->b_empty[i], 1);
+      mbar_init(&b->st_full[i], 1);
+      mbar_init(&b->st_empty[i], 1);
+      mbar_init(&b->s_full[i], 1);
+    }
+    mbar_init(&b->held_full, 1);
+    mbar_init(&b->held_empty, 1);
+    mbar_init(&b->p_full, 256);
+    mbar_init(&b->dp_full, 1);
+    mbar_init(&b->dp_read, 256);
+    mbar_init(&b->ds_full, 256);
+    mbar_init(&b->acc_full, 1);
   }
   for (int i = 0; i < 2; ++i) {
-    mbar_init(&b->b_full[i], 1);
-    mbar_init(&b->b_empty[i], 1);
-    mbar_init(&b->st_full[i], 1);
-    mbar_init(&b->st_empty[i], 1);
-    mbar_init(&b->s_full[i], 1);
+    mbar_init(&bars->item_full[i], 1);
+    mbar_init(&bars->item_empty[i], 9);  // the MMA warp and 8 softmax warps
   }
-  mbar_init(&b->held_full, 1);
-  mbar_init(&b->held_empty, 1);
-  mbar_init(&b->p_full, 256);
-  mbar_init(&b->dp_full, 1);
-  mbar_init(&b->dp_read, 256);
-  mbar_init(&b->ds_full, 256);
-  mbar_init(&b->acc_full, 1);
-  mbar_init(&b->drain, 1);
-  b->abort_flag = 0u;
+  mbar_init(&bars->smem_free, 1);
+  mbar_init(&bars->tmem_free, 256);
+  mbar_init(&bars->drain, 1);
+  bars->abort_flag = 0u;
   fence_barrier_init();
 }
 
@@ -172,30 +194,46 @@ __device__ __forceinline__ void bwd_store_row(uint32_t taddr, __nv_bfloat16* dst
   }
 }
 
-// ------------------------------------------------------------------------ dK and dV
+// ------------------------------------------------------------------------ the kernel
 //
-// Tensor memory: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [384,384+D): rows are KV tokens.
-// Tile n of an item (KV block, query blocks that keep it), in the MMA warp's issue order:
+// Items: every (head, KV block) for dK and dV, then every (head, query block) for dQ, taken in
+// order from a counter, so that a CTA whose list was short takes the next item sooner and the
+// dQ items fill the end of the dK/dV ones (lists of KV blocks differ in length by a factor of ten:
+// every query block keeps the text blocks). The load thread takes the items and hands them to the
+// other warps through two slots.
+//
+// dK, dV. Tensor memory: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [384,384+D): rows are KV
+// tokens. Issue order for tile n of an item:
 //   dV += P^T(n) dO(n);  S^T(n+1) = K Q(n+1)^T;  dK += dS^T(n) Q(n);  dP^T(n+1) = V dO(n+1)^T.
 // The softmax warps work on dS(n) while dV(n) and S(n+1) run, and on P(n+1) while dK(n) and
 // dP(n+1) run, so S, dP and the two accumulators need one buffer each (all 512 columns).
 // S(n+1) may overwrite P(n): tcgen05.mma of one thread run in order.
+//
+// dQ. Tensor memory: S of even and odd tiles [0,128), [128,256), dP [256,384), dQ [384,384+D): rows
+// are query tokens. Issue order per tile n: S(n+1) = Q K(n+1)^T; dP(n+1) = dO V(n+1)^T once dP(n) is
+// in registers; dQ += dS(n) K(n), with dS(n) over S(n). The softmax warps never wait for a product
+// that starts after their own previous step.
+//
+// Between the two a CTA hands its shared memory over when its last dK/dV product is done and its
+// tensor memory when the last dV and dK rows have been read.
 template <int D, int B>
 __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
-    attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                    const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const BwdParams p) {
+    attn_bwd_kernel(const __grid_constant__ BwdMaps maps, const BwdParams p) {
   using C = BwdConfig<D, B>;
   constexpr int BPT = C::kBlocksPerTile;
+  constexpr uint32_t TB = C::kTileBytes;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* k_tile = smem;
-  uint8_t* v_tile = smem + C::kTileBytes;
-  uint8_t* q_ring = smem + 2 * C::kTileBytes;
-  uint8_t* do_ring = q_ring + C::kStagesA * C::kTileBytes;
-  uint8_t* st_ring = do_ring + C::kStagesB * C::kTileBytes;
+  uint8_t* held0 = smem;                                // K, or Q
+  uint8_t* held1 = smem + TB;                           // V, or dO
+  uint8_t* ring_a = smem + 2 * TB;                      // Q, or K
+  uint8_t* ring_b = ring_a + C::kStagesA * TB;          // dO, or V
+  uint8_t* st_ring = ring_b + C::kStagesB * TB;         // lse and delta of the walked query rows
   BwdBars* bars = reinterpret_cast<BwdBars*>(st_ring + C::kStagesStat * C::kStatBytes);
+  BwdPhaseBars* bk = &bars->dkv;
+  BwdPhaseBars* bq = &bars->dq;
   volatile uint32_t* abort_flag = &bars->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n_all = p.n_dkv + p.n_dq;
 
   // The swizzled tiles need a 1024-byte aligned base, which this kernel's shared memory has
   // (it declares no static array); were it ever otherwise, nothing is computed and it is reported.
@@ -212,22 +250,20 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
-  constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;
+  constexpr uint32_t kS = 0, kDPk = 128, kDV = 256, kDK = 384;  // dK, dV items
+  constexpr uint32_t kDPq = 256, kDQ = 384;                     // dQ items
 
-  struct Item {
-    int h, j, n_ent, n_tiles;
-    const int32_t* rows;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
   };
-  auto get = [&](int item) {
-    Item it;
-    it.h = item / p.nkb;
-    it.j = item - it.h * p.nkb;
-    const int32_t* at = p.col_at + static_cast<int64_t>(it.h) * (p.nkb + 1) + it.j;
-    const int a = __ldg(at), b = __ldg(at + 1);
-    it.n_ent = b - a;
-    it.n_tiles = (it.n_ent + BPT - 1) / BPT;
-    it.rows = p.col_row + static_cast<int64_t>(it.h) * p.nqb * p.kmax + a;
-    return it;
+  // The k-th item of this CTA, for the warps that do not take it themselves.
+  auto next_item = [&](uint32_t k, int* item, int* n_ent) -> bool {
+    if (!wait_all(&bars->item_full[k & 1u], (k >> 1) & 1u)) return false;
+    *item = *const_cast<volatile int32_t*>(&bars->item[k & 1u]);
+    *n_ent = *const_cast<volatile int32_t*>(&bars->n_ent[k & 1u]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[k & 1u]);
+    return true;
   };
 
   if (warp >= 8) {
@@ -236,148 +272,250 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
       // ---------------------------------------------------------- TMA producer
       if (lane == 0) {
         const uint64_t pol_held = l2_policy_evict_first(), pol_walk = l2_policy_evict_last();
-        uint32_t t = 0, held = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-          const Item it = get(item);
-          if (it.n_tiles == 0) continue;
-          ok = mbar_wait(&bars->held_empty, (held & 1u) ^ 1u, abort_flag, p.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bars->held_full, 2 * C::kTileBytes);
+        uint32_t tk = 0, tq = 0, hk = 0, hq = 0;  // tiles and held pairs loaded in either phase
+        // A tile of one operand: `row[b]` is the first row of each of its boxes.
+        auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const int (&blk)[BPT], int h) {
+          mbar_arrive_expect_tx(bar, TB);
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+            for (int b = 0; b < BPT; ++b)
+              tma_load_3d_hint(smem_u32(dst) + c * C::kChunkBytes + b * C::kBoxBytes, map, bar, c * 64, blk[b] * B, h,
+                               pol_walk);
+        };
+        auto load_held = [&](BwdPhaseBars* pb, uint32_t n, const CUtensorMap* m0, const CUtensorMap* m1, int blk,
+                             int h) -> bool {
+          if (!mbar_wait(&pb->held_empty, (n & 1u) ^ 1u, abort_flag, p.status)) return false;
+          mbar_arrive_expect_tx(&pb->held_full, 2 * TB);
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c) {
-            tma_load_3d_hint(smem_u32(k_tile) + c * C::kChunkBytes, &tm_k, &bars->held_full, c * 64, it.j * B, it.h,
-                             pol_held);
-            tma_load_3d_hint(smem_u32(v_tile) + c * C::kChunkBytes, &tm_v, &bars->held_full, c * 64, it.j * B, it.h,
-                             pol_held);
+            tma_load_3d_hint(smem_u32(held0) + c * C::kChunkBytes, m0, &pb->held_full, c * 64, blk * B, h, pol_held);
+            tma_load_3d_hint(smem_u32(held1) + c * C::kChunkBytes, m1, &pb->held_full, c * 64, blk * B, h, pol_held);
           }
-          ++held;
-          for (int n = 0; n < it.n_tiles; ++n, ++t) {
-            int qb[BPT];
-#pragma unroll
-            for (int b = 0; b < BPT; ++b) {
-              const int e = n * BPT + b;
-              qb[b] = __ldg(it.rows + (e < it.n_ent ? e : n * BPT));
-            }
-            const uint32_t sa = t % C::kStagesA, sb = t % C::kStagesB;
-            ok = mbar_wait(&bars->st_empty[sb], ((t / 2) & 1u) ^ 1u, abort_flag, p.status);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&bars->st_full[sb], C::kStatBytes);
-            const uint32_t st = smem_u32(st_ring) + sb * C::kStatBytes;
-#pragma unroll
-            for (int b = 0; b < BPT; ++b) {
-              const int64_t at = (static_cast<int64_t>(it.h) * p.nqb + qb[b]) * B;
-              bulk_load(st + b * B * 4, p.lse2 + at, B * 4, &bars->st_full[sb]);
-              bulk_load(st + 512 + b * B * 4, p.delta + at, B * 4, &bars->st_full[sb]);
-            }
-            ok = mbar_wait(&bars->a_empty[sa], ((t / C::kStagesA) & 1u) ^ 1u, abort_flag, p.status);
-            if (!ok) {
-              bwd_drain(&bars->st_full[sb], (t / 2) & 1u);
-              break;
-            }
-            mbar_arrive_expect_tx(&bars->a_full[sa], C::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-              for (int b = 0; b < BPT; ++b)
-                tma_load_3d_hint(smem_u32(q_ring) + sa * C::kTileBytes + c * C::kChunkBytes + b * C::kBoxBytes, &tm_q,
-                                 &bars->a_full[sa], c * 64, qb[b] * B, it.h, pol_walk);
-            ok = mbar_wait(&bars->b_empty[sb], ((t / 2) & 1u) ^ 1u, abort_flag, p.status);
-            if (!ok) {
-              bwd_drain(&bars->st_full[sb], (t / 2) & 1u);
-              bwd_drain(&bars->a_full[sa], (t / C::kStagesA) & 1u);
-              break;
-            }
-            mbar_arrive_expect_tx(&bars->b_full[sb], C::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-              for (int b = 0; b < BPT; ++b)
-                tma_load_3d_hint(smem_u32(do_ring) + sb * C::kTileBytes + c * C::kChunkBytes + b * C::kBoxBytes, &tm_do,
-                                 &bars->b_full[sb], c * 64, qb[b] * B, it.h, pol_walk);
+          return true;
+        };
+        bool ok = true, in_dq = false;
+        int item = atomicAdd(p.next, 1);
+        for (uint32_t k = 0; ok; ++k) {
+          int n_ent = 0, h = 0, blk = 0;
+          const int32_t* list = nullptr;
+          if (item < p.n_dkv) {
+            h = item / p.nkb;
+            blk = item - h * p.nkb;
+            const int32_t* at = p.col_at + static_cast<int64_t>(h) * (p.nkb + 1) + blk;
+            const int a = __ldg(at);
+            n_ent = __ldg(at + 1) - a;
+            list = p.col_row + static_cast<int64_t>(h) * p.nqb * p.kmax + a;
+          } else if (item < n_all) {
+            const int iq = item - p.n_dkv;
+            h = iq / p.nqb;
+            blk = iq - h * p.nqb;
+            n_ent = bwd_count(__ldg(p.cnt + iq), p.kmax);
+            list = p.idx + static_cast<int64_t>(iq) * p.kmax;
           }
+          if (!mbar_wait(&bars->item_empty[k & 1u], ((k >> 1) & 1u) ^ 1u, abort_flag, p.status)) break;
+          *const_cast<volatile int32_t*>(&bars->item[k & 1u]) = item;
+          *const_cast<volatile int32_t*>(&bars->n_ent[k & 1u]) = n_ent;
+          mbar_arrive(&bars->item_full[k & 1u]);
+          if (item >= n_all) break;
+          const int n_tiles = (n_ent + BPT - 1) / BPT;
+          int taken = -1;
+          if (item < p.n_dkv) {
+            if (n_tiles > 0) {
+              if (!(ok = load_held(bk, hk, &maps.held[2], &maps.held[3], blk, h))) break;
+              ++hk;
+            }
+            for (int n = 0; n < n_tiles; ++n, ++tk) {
+              if (n == n_tiles - 1) taken = atomicAdd(p.next, 1);  // in time for the item after this one
+              int qb[BPT];
+#pragma unroll
+              for (int b = 0; b < BPT; ++b) {
+                const int e = n * BPT + b;
+                qb[b] = __ldg(list + (e < n_ent ? e : n * BPT));
+              }
+              const uint32_t sa = tk % C::kStagesA, sb = tk % C::kStagesB;
+              if (!(ok = mbar_wait(&bk->st_empty[sb], ((tk / 2) & 1u) ^ 1u, abort_flag, p.status))) break;
+              mbar_arrive_expect_tx(&bk->st_full[sb], C::kStatBytes);
+              const uint32_t st = smem_u32(st_ring) + sb * C::kStatBytes;
+#pragma unroll
+              for (int b = 0; b < BPT; ++b) {
+                const int64_t at = (static_cast<int64_t>(h) * p.nqb + qb[b]) * B;
+                bulk_load(st + b * B * 4, p.lse2 + at, B * 4, &bk->st_full[sb]);
+                bulk_load(st + 512 + b * B * 4, p.delta + at, B * 4, &bk->st_full[sb]);
+              }
+              if (!(ok = mbar_wait(&bk->a_empty[sa], ((tk / C::kStagesA) & 1u) ^ 1u, abort_flag, p.status))) {
+                bwd_drain(&bk->st_full[sb], (tk / 2) & 1u);
+                break;
+              }
+              load_tile(ring_a + sa * TB, &maps.walk[0], &bk->a_full[sa], qb, h);
+              if (!(ok = mbar_wait(&bk->b_empty[sb], ((tk / C::kStagesB) & 1u) ^ 1u, abort_flag, p.status))) {
+                bwd_drain(&bk->st_full[sb], (tk / 2) & 1u);
+                bwd_drain(&bk->a_full[sa], (tk / C::kStagesA) & 1u);
+                break;
+              }
+              load_tile(ring_b + sb * TB, &maps.walk[1], &bk->b_full[sb], qb, h);
+            }
+          } else {
+            if (!in_dq) {  // the last dK/dV product has read its tiles
+              in_dq = true;
+              if (!(ok = mbar_wait(&bars->smem_free, 0u, abort_flag, p.status))) break;
+            }
+            if (!(ok = load_held(bq, hq, &maps.held[0], &maps.held[1], blk, h))) break;
+            ++hq;
+            for (int n = 0; n < n_tiles; ++n, ++tq) {
+              if (n == n_tiles - 1) taken = atomicAdd(p.next, 1);
+              int jb[BPT];
+#pragma unroll
+              for (int b = 0; b < BPT; ++b) {
+                const int e = n * BPT + b;
+                jb[b] = bwd_block(__ldg(list + (e < n_ent ? e : n * BPT)), p.nkb);
+              }
+              const uint32_t sa = tq % C::kStagesA, sb = tq % C::kStagesB;
+              if (!(ok = mbar_wait(&bq->a_empty[sa], ((tq / C::kStagesA) & 1u) ^ 1u, abort_flag, p.status))) break;
+              load_tile(ring_a + sa * TB, &maps.walk[2], &bq->a_full[sa], jb, h);
+              if (!(ok = mbar_wait(&bq->b_empty[sb], ((tq / C::kStagesB) & 1u) ^ 1u, abort_flag, p.status))) {
+                bwd_drain(&bq->a_full[sa], (tq / C::kStagesA) & 1u);
+                break;
+              }
+              load_tile(ring_b + sb * TB, &maps.walk[3], &bq->b_full[sb], jb, h);
+            }
+          }
+          item = taken >= 0 ? taken : atomicAdd(p.next, 1);
         }
         // every copy lands before the CTA exits (matters only after an abort)
-        if (held > 0) bwd_drain(&bars->held_full, (held - 1) & 1u);
-        bwd_drain_ring(bars->st_full, 2, t);
-        bwd_drain_ring(bars->a_full, C::kStagesA, t);
-        bwd_drain_ring(bars->b_full, C::kStagesB, t);
+        if (hk > 0) bwd_drain(&bk->held_full, (hk - 1) & 1u);
+        if (hq > 0) bwd_drain(&bq->held_full, (hq - 1) & 1u);
+        bwd_drain_ring(bk->st_full, 2, tk);
+        bwd_drain_ring(bk->a_full, C::kStagesA, tk);
+        bwd_drain_ring(bk->b_full, C::kStagesB, tk);
+        bwd_drain_ring(bq->a_full, C::kStagesA, tq);
+        bwd_drain_ring(bq->b_full, C::kStagesB, tq);
       }
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
-      };
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(k_tile), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(v_tile), 16, 1024);
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(q_ring), 16, 1024);
-      const uint64_t do_desc = smem_desc_sw128(smem_u32(do_ring), 16, 1024);
-      const uint64_t q_mn = smem_desc_sw128(smem_u32(q_ring), C::kChunkBytes, 1024);
-      const uint64_t do_mn = smem_desc_sw128(smem_u32(do_ring), C::kChunkBytes, 1024);
-      auto product = [&](uint32_t d, uint64_t a, uint64_t b) {
+      // K-major views of every tile, and the MN-major ones of the walked tiles
+      const uint64_t h0 = smem_desc_sw128(smem_u32(held0), 16, 1024);
+      const uint64_t h1 = smem_desc_sw128(smem_u32(held1), 16, 1024);
+      const uint64_t ra = smem_desc_sw128(smem_u32(ring_a), 16, 1024);
+      const uint64_t rb = smem_desc_sw128(smem_u32(ring_b), 16, 1024);
+      const uint64_t ra_mn = smem_desc_sw128(smem_u32(ring_a), C::kChunkBytes, 1024);
+      const uint64_t rb_mn = smem_desc_sw128(smem_u32(ring_b), C::kChunkBytes, 1024);
+      auto product = [&](uint32_t d, uint64_t a, uint64_t b) {  // 128 x 128 over D
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
           mma_ss(d, a + off, b + off, C::kIdescS, kk > 0 ? 1u : 0u);
         }
       };
-      auto gather = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {
+      auto gather = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {  // 128 x D over 128 rows
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(d, a + bwd_a_col(kk), b + ((kk * 2048) >> 4), C::kIdescAcc, (add || kk > 0) ? 1u : 0u);
       };
-      uint32_t t = 0, held = 0;
-      bool ok = true;
-      auto issue_s = [&](uint32_t u) -> bool {
+      auto stage_of = [&](uint32_t st) { return static_cast<uint64_t>((st * TB) >> 4); };
+      uint32_t tk = 0, tq = 0, hk = 0, hq = 0;
+      bool ok = true, in_dq = false;
+      auto k_issue_s = [&](uint32_t u) -> bool {
         const uint32_t sa = u % C::kStagesA;
-        if (!wait_all(&bars->a_full[sa], (u / C::kStagesA) & 1u)) return false;
+        if (!wait_all(&bk->a_full[sa], (u / C::kStagesA) & 1u)) return false;
         if (elect_one()) {
-          product(tmem + kS, k_desc, q_desc + ((sa * C::kTileBytes) >> 4));
-          mma_commit(&bars->s_full[0]);
+          product(tmem + kS, h0, ra + stage_of(sa));
+          mma_commit(&bk->s_full[0]);
         }
         __syncwarp();
         return true;
       };
-      auto issue_dp = [&](uint32_t u, bool last) -> bool {
+      auto k_issue_dp = [&](uint32_t u, bool last) -> bool {
         const uint32_t sb = u % C::kStagesB;
-        if (!wait_all(&bars->b_full[sb], (u / C::kStagesB) & 1u)) return false;
+        if (!wait_all(&bk->b_full[sb], (u / C::kStagesB) & 1u)) return false;
         if (elect_one()) {
-          product(tmem + kDP, v_desc, do_desc + ((sb * C::kTileBytes) >> 4));
-          mma_commit(&bars->dp_full);
-          if (last) mma_commit(&bars->held_empty);
+          product(tmem + kDPk, h1, rb + stage_of(sb));
+          mma_commit(&bk->dp_full);
+          if (last) mma_commit(&bk->held_empty);
         }
         __syncwarp();
         return true;
       };
-      for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-        const Item it = get(item);
-        if (it.n_tiles == 0) continue;
-        ok = wait_all(&bars->held_full, held & 1u);
-        if (!ok) break;
-        ++held;
-        ok = issue_s(t) && issue_dp(t, it.n_tiles == 1);
-        for (int n = 0; ok && n < it.n_tiles; ++n, ++t) {
-          const bool last = n == it.n_tiles - 1;
-          const uint32_t sa = t % C::kStagesA, sb = t % C::kStagesB;
-          if (!(ok = wait_all(&bars->p_full, t & 1u))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            gather(tmem + kDV, tmem + kS, do_mn + ((sb * C::kTileBytes) >> 4), n > 0);
-            mma_commit(&bars->b_empty[sb]);
+      auto q_issue_s = [&](uint32_t u) -> bool {
+        const uint32_t sa = u % C::kStagesA;
+        if (!wait_all(&bq->a_full[sa], (u / C::kStagesA) & 1u)) return false;
+        if (elect_one()) {
+          product(tmem + kS + 128u * (u & 1u), h0, ra + stage_of(sa));
+          mma_commit(&bq->s_full[u & 1u]);
+        }
+        __syncwarp();
+        return true;
+      };
+      auto q_issue_dp = [&](uint32_t u, bool last) -> bool {
+        const uint32_t sb = u % C::kStagesB;
+        if (u > 0 && !wait_all(&bq->dp_read, (u - 1) & 1u)) return false;
+        if (!wait_all(&bq->b_full[sb], (u / C::kStagesB) & 1u)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+          product(tmem + kDPq, h1, rb + stage_of(sb));
+          mma_commit(&bq->dp_full);
+          mma_commit(&bq->b_empty[sb]);
+          if (last) mma_commit(&bq->held_empty);
+        }
+        __syncwarp();
+        return true;
+      };
+      for (uint32_t k = 0; ok; ++k) {
+        int item, n_ent;
+        if (!next_item(k, &item, &n_ent) || item >= n_all) break;
+        const int n_tiles = (n_ent + BPT - 1) / BPT;
+        if (item < p.n_dkv) {
+          if (n_tiles == 0) continue;
+          if (!(ok = wait_all(&bk->held_full, hk & 1u))) break;
+          ++hk;
+          ok = k_issue_s(tk) && k_issue_dp(tk, n_tiles == 1);
+          for (int n = 0; ok && n < n_tiles; ++n, ++tk) {
+            const bool last = n == n_tiles - 1;
+            const uint32_t sa = tk % C::kStagesA, sb = tk % C::kStagesB;
+            if (!(ok = wait_all(&bk->p_full, tk & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              gather(tmem + kDV, tmem + kS, rb_mn + stage_of(sb), n > 0);
+              mma_commit(&bk->b_empty[sb]);
+            }
+            __syncwarp();
+            if (!last && !(ok = k_issue_s(tk + 1))) break;
+            if (!(ok = wait_all(&bk->ds_full, tk & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              gather(tmem + kDK, tmem + kDPk, ra_mn + stage_of(sa), n > 0);
+              mma_commit(&bk->a_empty[sa]);
+              mma_commit(&bk->st_empty[sb]);
+              if (last) mma_commit(&bk->acc_full);
+            }
+            __syncwarp();
+            if (!last && !(ok = k_issue_dp(tk + 1, n == n_tiles - 2))) break;
           }
-          __syncwarp();
-          if (!last && !(ok = issue_s(t + 1))) break;
-          if (!(ok = wait_all(&bars->ds_full, t & 1u))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            gather(tmem + kDK, tmem + kDP, q_mn + ((sa * C::kTileBytes) >> 4), n > 0);
-            mma_commit(&bars->a_empty[sa]);
-            mma_commit(&bars->st_empty[sb]);
-            if (last) mma_commit(&bars->acc_full);
+        } else {
+          if (!in_dq) {
+            in_dq = true;
+            if (elect_one()) mma_commit(&bars->smem_free);
+            __syncwarp();
+            if (!(ok = wait_all(&bars->tmem_free, 0u))) break;
+            tc_fence_after();
           }
-          __syncwarp();
-          if (!last && !(ok = issue_dp(t + 1, n == it.n_tiles - 2))) break;
+          if (!(ok = wait_all(&bq->held_full, hq & 1u))) break;
+          ++hq;
+          ok = q_issue_s(tq) && q_issue_dp(tq, n_tiles == 1);
+          for (int n = 0; ok && n < n_tiles; ++n, ++tq) {
+            const bool last = n == n_tiles - 1;
+            if (!last && !(ok = q_issue_s(tq + 1) && q_issue_dp(tq + 1, n == n_tiles - 2))) break;
+            if (!(ok = wait_all(&bq->ds_full, tq & 1u))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t sa = tq % C::kStagesA;
+              gather(tmem + kDQ, tmem + kS + 128u * (tq & 1u), ra_mn + stage_of(sa), n > 0);
+              mma_commit(&bq->a_empty[sa]);
+              if (last) mma_commit(&bq->acc_full);
+            }
+            __syncwarp();
+          }
         }
       }
       if (elect_one()) mma_commit(&bars->drain);
@@ -387,350 +525,158 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
     }  // warps 10 and 11 only complete the warpgroup
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    // ---------------------------------------------------------- P, dS and the epilogue
+    // ---------------------------------------------------------- P, dS and the epilogues
     const int half = warp >> 2, wq = warp & 3;
-    const int row = wq * 32 + lane;  // KV token of the block
+    const int row = wq * 32 + lane;  // row of the held block: KV token, or query token
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + kS + 64 * half, t_dp = tmem + lane_off + kDP + 64 * half;
-    uint32_t t = 0, done = 0;
-    bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
-    };
-    for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-      const Item it = get(item);
-      const int64_t tok = static_cast<int64_t>(it.j) * B + row;
-      const bool put = row < B && tok < p.n_kv;
-      __nv_bfloat16* dst = (half == 0 ? p.dv : p.dk) + (static_cast<int64_t>(it.h) * p.n_kv + tok) * D;
-      if (it.n_tiles == 0) {  // a block that no query block keeps
-        if (put)
-          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      // With 64-token blocks rows 64-127 belong to the next KV block: computed, never stored.
-      const bool idle = B < 128 && wq * 32 >= B;
-      for (int n = 0; n < it.n_tiles; ++n, ++t) {
-        const uint32_t sb = t & 1u;
-        const float4* lse = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + half * 256);
-        const float4* del = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + 512 + half * 256);
-        if (!(ok = wait_all(&bars->st_full[sb], (t >> 1) & 1u))) break;
-        if (!(ok = wait_all(&bars->s_full[0], t & 1u))) break;
-        if (idle) {
-          // whatever S and dP left there stands in for P and dS of rows that are dropped
-          mbar_arrive(&bars->p_full);
-          if (!(ok = wait_all(&bars->dp_full, t & 1u))) break;
-          mbar_arrive(&bars->ds_full);
-          continue;
-        }
-        tc_fence_after();
-        uint32_t r[2][32];
-        float pr[64];
-        bwd_load_half(t_s, r);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 l = lse[e];
-          const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 4 * e + i;
-            pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, -lv[i]));
-          }
-        }
-        if (BPT > 1 && half == 1 && 2 * n + 1 >= it.n_ent) {  // odd last entry: its half repeats a block
-#pragma unroll
-          for (int c = 0; c < 64; ++c) pr[c] = 0.f;
-        }
-        bwd_store_half(t_s, pr);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->p_full);
-        if (!(ok = wait_all(&bars->dp_full, t & 1u))) break;
-        tc_fence_after();
-        bwd_load_half(t_dp, r);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 l = del[e];
-          const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 4 * e + i;
-            pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - lv[i];
-          }
-        }
-        bwd_store_half(t_dp, pr);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&bars->ds_full);
-      }
-      if (!ok) break;
-      if (!(ok = wait_all(&bars->acc_full, done & 1u))) break;
-      ++done;
-      tc_fence_after();
-      if (!idle) bwd_store_row<D>(tmem + lane_off + (half == 0 ? kDV : kDK), dst, put, half == 0 ? 1.f : p.scale);
-      tc_fence_before();
-    }
-  }
-
-  tc_fence_before();
-  __syncthreads();
-  if (warp == C::kMmaWarp) {
-    tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
-  }
-}
-
-// ------------------------------------------------------------------------ dQ
-//
-// Tensor memory: S of even and odd tiles [0,128), [128,256), dP [256,384), dQ [384,384+D): rows are
-// query tokens. Issue order per tile n: S(n+1) = Q K(n+1)^T; dP(n+1) = dO V(n+1)^T once dP(n) is in
-// registers; dQ += dS(n) K(n), with dS(n) over S(n). The softmax warps never wait for a product
-// that starts after their own previous step.
-template <int D, int B>
-__global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
-    attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                   const BwdParams p) {
-  using C = BwdConfig<D, B>;
-  constexpr int BPT = C::kBlocksPerTile;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* q_tile = smem;
-  uint8_t* do_tile = smem + C::kTileBytes;
-  uint8_t* k_ring = smem + 2 * C::kTileBytes;
-  uint8_t* v_ring = k_ring + C::kStagesA * C::kTileBytes;
-  BwdBars* bars = reinterpret_cast<BwdBars*>(v_ring + C::kStagesB * C::kTileBytes);
-  volatile uint32_t* abort_flag = &bars->abort_flag;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  if ((smem_u32(smem) & 1023u) != 0u) {
-    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
-    return;
-  }
-  if (threadIdx.x == 0) bwd_bars_init(bars);
-  if (warp == C::kMmaWarp) {
-    tmem_alloc(&bars->tmem, C::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = bars->tmem;
-  constexpr uint32_t kS = 0, kDP = 256, kDQ = 384;
-
-  auto tiles_of = [&](int item, int* n_ent) {
-    *n_ent = bwd_count(__ldg(p.cnt + item), p.kmax);
-    return (*n_ent + BPT - 1) / BPT;
-  };
-
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsProducer));
-    if (warp == C::kLoadWarp) {
-      // ---------------------------------------------------------- TMA producer
-      if (lane == 0) {
-        const uint64_t pol_held = l2_policy_evict_first(), pol_walk = l2_policy_evict_last();
-        uint32_t t = 0, held = 0;
-        bool ok = true;
-        for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-          const int h = item / p.nqb, qb = item - h * p.nqb;
-          int n_ent;
-          const int n_tiles = tiles_of(item, &n_ent);
-          const int32_t* list = p.idx + static_cast<int64_t>(item) * p.kmax;
-          ok = mbar_wait(&bars->held_empty, (held & 1u) ^ 1u, abort_flag, p.status);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&bars->held_full, 2 * C::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c) {
-            tma_load_3d_hint(smem_u32(q_tile) + c * C::kChunkBytes, &tm_q, &bars->held_full, c * 64, qb * B, h,
-                             pol_held);
-            tma_load_3d_hint(smem_u32(do_tile) + c * C::kChunkBytes, &tm_do, &bars->held_full, c * 64, qb * B, h,
-                             pol_held);
-          }
-          ++held;
-          for (int n = 0; n < n_tiles; ++n, ++t) {
-            int jb[BPT];
-#pragma unroll
-            for (int b = 0; b < BPT; ++b) {
-              const int e = n * BPT + b;
-              jb[b] = bwd_block(__ldg(list + (e < n_ent ? e : n * BPT)), p.nkb);
-            }
-            const uint32_t sa = t % C::kStagesA, sb = t % C::kStagesB;
-            ok = mbar_wait(&bars->a_empty[sa], ((t / C::kStagesA) & 1u) ^ 1u, abort_flag, p.status);
-            if (!ok) break;
-            mbar_arrive_expect_tx(&bars->a_full[sa], C::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-              for (int b = 0; b < BPT; ++b)
-                tma_load_3d_hint(smem_u32(k_ring) + sa * C::kTileBytes + c * C::kChunkBytes + b * C::kBoxBytes, &tm_k,
-                                 &bars->a_full[sa], c * 64, jb[b] * B, h, pol_walk);
-            ok = mbar_wait(&bars->b_empty[sb], ((t / C::kStagesB) & 1u) ^ 1u, abort_flag, p.status);
-            if (!ok) {
-              bwd_drain(&bars->a_full[sa], (t / C::kStagesA) & 1u);
-              break;
-            }
-            mbar_arrive_expect_tx(&bars->b_full[sb], C::kTileBytes);
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-              for (int b = 0; b < BPT; ++b)
-                tma_load_3d_hint(smem_u32(v_ring) + sb * C::kTileBytes + c * C::kChunkBytes + b * C::kBoxBytes, &tm_v,
-                                 &bars->b_full[sb], c * 64, jb[b] * B, h, pol_walk);
-          }
-        }
-        if (held > 0) bwd_drain(&bars->held_full, (held - 1) & 1u);
-        bwd_drain_ring(bars->a_full, C::kStagesA, t);
-        bwd_drain_ring(bars->b_full, C::kStagesB, t);
-      }
-      __syncwarp();
-    } else if (warp == C::kMmaWarp) {
-      // ---------------------------------------------------------- MMA issuer
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
-      };
-      const uint64_t q_desc = smem_desc_sw128(smem_u32(q_tile), 16, 1024);
-      const uint64_t do_desc = smem_desc_sw128(smem_u32(do_tile), 16, 1024);
-      const uint64_t k_desc = smem_desc_sw128(smem_u32(k_ring), 16, 1024);
-      const uint64_t v_desc = smem_desc_sw128(smem_u32(v_ring), 16, 1024);
-      const uint64_t k_mn = smem_desc_sw128(smem_u32(k_ring), C::kChunkBytes, 1024);
-      auto product = [&](uint32_t d, uint64_t a, uint64_t b) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4;
-          mma_ss(d, a + off, b + off, C::kIdescS, kk > 0 ? 1u : 0u);
-        }
-      };
-      uint32_t t = 0, held = 0;
-      bool ok = true;
-      auto issue_s = [&](uint32_t u) -> bool {
-        const uint32_t sa = u % C::kStagesA;
-        if (!wait_all(&bars->a_full[sa], (u / C::kStagesA) & 1u)) return false;
-        if (elect_one()) {
-          product(tmem + kS + 128u * (u & 1u), q_desc, k_desc + ((sa * C::kTileBytes) >> 4));
-          mma_commit(&bars->s_full[u & 1u]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_dp = [&](uint32_t u, bool last) -> bool {
-        const uint32_t sb = u % C::kStagesB;
-        if (u > 0 && !wait_all(&bars->dp_read, (u - 1) & 1u)) return false;
-        if (!wait_all(&bars->b_full[sb], (u / C::kStagesB) & 1u)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          product(tmem + kDP, do_desc, v_desc + ((sb * C::kTileBytes) >> 4));
-          mma_commit(&bars->dp_full);
-          mma_commit(&bars->b_empty[sb]);
-          if (last) mma_commit(&bars->held_empty);
-        }
-        __syncwarp();
-        return true;
-      };
-      for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-        int n_ent;
-        const int n_tiles = tiles_of(item, &n_ent);
-        ok = wait_all(&bars->held_full, held & 1u);
-        if (!ok) break;
-        ++held;
-        ok = issue_s(t) && issue_dp(t, n_tiles == 1);
-        for (int n = 0; ok && n < n_tiles; ++n, ++t) {
-          const bool last = n == n_tiles - 1;
-          if (!last && !(ok = issue_s(t + 1) && issue_dp(t + 1, n == n_tiles - 2))) break;
-          if (!(ok = wait_all(&bars->ds_full, t & 1u))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t sa = t % C::kStagesA;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tmem + kDQ, tmem + kS + 128u * (t & 1u) + bwd_a_col(kk),
-                     k_mn + ((sa * C::kTileBytes + kk * 2048) >> 4), C::kIdescAcc, (n > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&bars->a_empty[sa]);
-            if (last) mma_commit(&bars->acc_full);
-          }
-          __syncwarp();
-        }
-      }
-      if (elect_one()) mma_commit(&bars->drain);
-      __syncwarp();
-      bwd_drain(&bars->drain, 0);
-      __syncwarp();
-    }
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
-    // ---------------------------------------------------------- dS and the epilogue
-    const int half = warp >> 2, wq = warp & 3;
-    const int row = wq * 32 + lane;  // query token of the block
-    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    uint32_t t = 0, done = 0;
-    bool ok = true;
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
-    };
-    const bool ragged_kv = p.n_kv % B != 0;
+    // With 64-token blocks rows 64-127 of a held tile belong to the next block: whatever stands
+    // in their rows of P and dS only reaches accumulator rows that are never stored.
     const bool idle = B < 128 && wq * 32 >= B;
-    for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-      const int h = item / p.nqb, qb = item - h * p.nqb;
-      int n_ent;
-      const int n_tiles = tiles_of(item, &n_ent);
-      const int32_t* list = p.idx + static_cast<int64_t>(item) * p.kmax;
-      const int64_t tok = static_cast<int64_t>(qb) * B + row;
-      float neg_lse = 0.f, delta = 0.f;
-      if (row < B) {
-        const int64_t at = (static_cast<int64_t>(h) * p.nqb + qb) * B + row;
-        neg_lse = -__ldg(p.lse2 + at);
-        delta = __ldg(p.delta + at);
-      }
-      for (int n = 0; n < n_tiles; ++n, ++t) {
-        const uint32_t t_s = tmem + lane_off + kS + 128u * (t & 1u) + 64 * half;
-        const uint32_t t_dp = tmem + lane_off + kDP + 64 * half;
-        // valid columns of this half of the tile
-        int nv = 64;
-        if (BPT > 1 && half == 1 && 2 * n + 1 >= n_ent) nv = 0;  // odd last entry: its half repeats a block
-        if (ragged_kv && nv > 0) {
-          const int j = bwd_block(__ldg(list + (BPT > 1 ? 2 * n + half : n)), p.nkb);
-          if (j == p.nkb - 1) {
-            const int64_t left = p.n_kv - static_cast<int64_t>(j) * B - (BPT > 1 ? 0 : 64 * half);
-            nv = left < 0 ? 0 : left < 64 ? static_cast<int>(left) : 64;
-          }
-        }
-        if (!(ok = wait_all(&bars->s_full[t & 1u], (t >> 1) & 1u))) break;
-        if (idle) {
-          if (!(ok = wait_all(&bars->dp_full, t & 1u))) break;
-          mbar_arrive(&bars->dp_read);
-          mbar_arrive(&bars->ds_full);
+    const bool ragged_kv = p.n_kv % B != 0;
+    uint32_t tk = 0, tq = 0, dk_done = 0, dq_done = 0;
+    bool ok = true, in_dq = false;
+    for (uint32_t k = 0; ok; ++k) {
+      int item, n_ent;
+      if (!next_item(k, &item, &n_ent) || item >= n_all) break;
+      const int n_tiles = (n_ent + BPT - 1) / BPT;
+      if (item < p.n_dkv) {
+        const int h = item / p.nkb, blk = item - h * p.nkb;
+        const int64_t tok = static_cast<int64_t>(blk) * B + row;
+        const bool put = row < B && tok < p.n_kv;
+        __nv_bfloat16* dst = (half == 0 ? p.dv : p.dk) + (static_cast<int64_t>(h) * p.n_kv + tok) * D;
+        if (n_tiles == 0) {  // a block that no query block keeps
+          if (put)
+            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0u, 0u, 0u, 0u);
           continue;
         }
-        tc_fence_after();
-        uint32_t r[2][32];
-        float pr[64];
-        bwd_load_half(t_s, r);
+        const uint32_t t_s = tmem + lane_off + kS + 64 * half, t_dp = tmem + lane_off + kDPk + 64 * half;
+        for (int n = 0; n < n_tiles; ++n, ++tk) {
+          const uint32_t sb = tk & 1u;
+          const float4* lse = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + half * 256);
+          const float4* del = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + 512 + half * 256);
+          if (!(ok = wait_all(&bk->st_full[sb], (tk >> 1) & 1u))) break;
+          if (!(ok = wait_all(&bk->s_full[0], tk & 1u))) break;
+          if (idle) {
+            mbar_arrive(&bk->p_full);
+            if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
+            mbar_arrive(&bk->ds_full);
+            continue;
+          }
+          tc_fence_after();
+          uint32_t r[2][32];
+          float pr[64];
+          bwd_load_half(t_s, r);
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
-          pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, neg_lse));
-        if (nv < 64) {
+          for (int e = 0; e < 16; ++e) {
+            const float4 l = lse[e];
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 4 * e + i;
+              pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, -lv[i]));
+            }
+          }
+          if (BPT > 1 && half == 1 && 2 * n + 1 >= n_ent) {  // odd last entry: its half repeats a block
+#pragma unroll
+            for (int c = 0; c < 64; ++c) pr[c] = 0.f;
+          }
+          bwd_store_half(t_s, pr);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bk->p_full);
+          if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
+          tc_fence_after();
+          bwd_load_half(t_dp, r);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float4 l = del[e];
+            const float lv[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 4 * e + i;
+              pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - lv[i];
+            }
+          }
+          bwd_store_half(t_dp, pr);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bk->ds_full);
+        }
+        if (!ok) break;
+        if (!(ok = wait_all(&bk->acc_full, dk_done & 1u))) break;
+        ++dk_done;
+        tc_fence_after();
+        if (!idle) bwd_store_row<D>(tmem + lane_off + (half == 0 ? kDV : kDK), dst, put, half == 0 ? 1.f : p.scale);
+        tc_fence_before();
+      } else {
+        const int iq = item - p.n_dkv, h = iq / p.nqb, blk = iq - h * p.nqb;
+        if (!in_dq) {
+          in_dq = true;
+          tc_fence_before();
+          mbar_arrive(&bars->tmem_free);
+        }
+        const int32_t* list = p.idx + static_cast<int64_t>(iq) * p.kmax;
+        const int64_t tok = static_cast<int64_t>(blk) * B + row;
+        float neg_lse = 0.f, delta = 0.f;
+        if (row < B) {
+          const int64_t at = static_cast<int64_t>(iq) * B + row;
+          neg_lse = -__ldg(p.lse2 + at);
+          delta = __ldg(p.delta + at);
+        }
+        for (int n = 0; n < n_tiles; ++n, ++tq) {
+          const uint32_t t_s = tmem + lane_off + kS + 128u * (tq & 1u) + 64 * half;
+          const uint32_t t_dp = tmem + lane_off + kDPq + 64 * half;
+          // valid columns of this half of the tile
+          int nv = 64;
+          if (BPT > 1 && half == 1 && 2 * n + 1 >= n_ent) nv = 0;  // odd last entry: its half repeats a block
+          if (ragged_kv && nv > 0) {
+            const int j = bwd_block(__ldg(list + (BPT > 1 ? 2 * n + half : n)), p.nkb);
+            if (j == p.nkb - 1) {
+              const int64_t left = p.n_kv - static_cast<int64_t>(j) * B - (BPT > 1 ? 0 : 64 * half);
+              nv = left < 0 ? 0 : left < 64 ? static_cast<int>(left) : 64;
+            }
+          }
+          if (!(ok = wait_all(&bq->s_full[tq & 1u], (tq >> 1) & 1u))) break;
+          if (idle) {
+            if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
+            mbar_arrive(&bq->dp_read);
+            mbar_arrive(&bq->ds_full);
+            continue;
+          }
+          tc_fence_after();
+          uint32_t r[2][32];
+          float pr[64];
+          bwd_load_half(t_s, r);
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (c >= nv) pr[c] = 0.f;
-        }
-        if (!(ok = wait_all(&bars->dp_full, t & 1u))) break;
-        tc_fence_after();
-        bwd_load_half(t_dp, r);
-        tc_fence_before();
-        mbar_arrive(&bars->dp_read);
+            pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, neg_lse));
+          if (nv < 64) {
 #pragma unroll
-        for (int c = 0; c < 64; ++c) pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - delta;
-        bwd_store_half(t_s, pr);
-        tmem_wait_st();
+            for (int c = 0; c < 64; ++c)
+              if (c >= nv) pr[c] = 0.f;
+          }
+          if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
+          tc_fence_after();
+          bwd_load_half(t_dp, r);
+          tc_fence_before();
+          mbar_arrive(&bq->dp_read);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - delta;
+          bwd_store_half(t_s, pr);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bq->ds_full);
+        }
+        if (!ok) break;
+        if (!(ok = wait_all(&bq->acc_full, dq_done & 1u))) break;
+        ++dq_done;
+        tc_fence_after();
+        const bool put = row < B && tok < p.n_q;
+        if (!idle)
+          bwd_store_row<D / 2>(tmem + lane_off + kDQ + (D / 2) * half,
+                               p.dq + (static_cast<int64_t>(h) * p.n_q + tok) * D + (D / 2) * half, put, p.scale);
         tc_fence_before();
-        mbar_arrive(&bars->ds_full);
       }
-      if (!ok) break;
-      if (!(ok = wait_all(&bars->acc_full, done & 1u))) break;
-      ++done;
-      tc_fence_after();
-      const bool put = row < B && tok < p.n_q;
-      if (!idle)
-        bwd_store_row<D / 2>(tmem + lane_off + kDQ + (D / 2) * half,
-                             p.dq + (static_cast<int64_t>(h) * p.n_q + tok) * D + (D / 2) * half, put, p.scale);
-      tc_fence_before();
     }
   }
 
@@ -751,8 +697,9 @@ template <int D>
 __global__ void __launch_bounds__(256)
     bwd_rows_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ d_o,
                     const float* __restrict__ lse, int64_t n_q, int64_t n_pad, float* __restrict__ lse2,
-                    float* __restrict__ delta) {
+                    float* __restrict__ delta, int* __restrict__ next) {
   constexpr int G = D / 8;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *next = 0;  // the item counter of this call
   const int l = threadIdx.x % G;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
   const int64_t h = blockIdx.y;

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -435,8 +436,7 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous()):
             raise ValueError(f"{name} must be contiguous bf16 {list(like.shape)}")
-    _check_same_device(q.device, do=do, k=k, v=v, o=o, lse=lse, idx=idx, cnt=cnt, dq=dq, dk=dk, dv=dv,
-                       workspace=None if workspace is None else workspace.buf)
+    _check_device(q.device, do, k, v, o, lse, idx, cnt, dq, dk, dv, None if workspace is None else workspace.buf)
     kmax = max(int(idx.shape[-1]), 1)
     with _launch(q.device, stream) as st:
         dq = torch.empty_like(q) if dq is None else dq
@@ -452,62 +452,70 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
 
 # ------------------------------------------------------------------ norm, rotation, head layout
 
-@contextlib.contextmanager
-def _launch(device: torch.device, stream):
+class _launch:
     """Makes `device` and `stream` (None: the device's current stream) current, so that buffers
-    allocated inside belong to the stream that uses them. Yields the stream's pointer."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield int(torch.cuda.current_stream().cuda_stream) or None
-        else:
-            with torch.cuda.stream(stream):
-                yield int(stream.cuda_stream) or None
+    allocated inside belong to the stream that uses them; gives the stream's pointer. Where they
+    are current already, which is the usual call, nothing is switched."""
+
+    __slots__ = ("device", "stream", "switched")
+
+    def __init__(self, device: torch.device, stream):
+        self.device, self.stream, self.switched = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None or torch.cuda.current_device() != self.device.index:
+            self.switched = contextlib.ExitStack()
+            self.switched.enter_context(torch.cuda.device(self.device))
+            if self.stream is not None:
+                self.switched.enter_context(torch.cuda.stream(self.stream))
+        return int((self.stream or torch.cuda.current_stream()).cuda_stream) or None
+
+    def __exit__(self, *exc):
+        if self.switched is not None:
+            self.switched.close()
 
 
-def _check_same_device(device, **tensors):
+def _check_device(device, *tensors):
+    """All of `tensors` (None: left out) on one CUDA device."""
     if device.type != "cuda":
         raise ValueError("tensors must be CUDA tensors")
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+            raise ValueError(f"tensors are on {device} and {t.device}")
 
 
 _NO_VIEW = View(None, 0, 0, 0)
 
 
-def _stride(t: torch.Tensor, dim: int) -> int:
-    return t.stride(dim) if t.shape[dim] > 1 else t.shape[-1]
-
-
-def _view(t: Optional[torch.Tensor], token: int, head: int, seq: Optional[int] = None) -> View:
+def _view(name: str, t: Optional[torch.Tensor], shape, dtype, token: int, head: int, seq: int = -1) -> View:
+    """The strided head vectors of t (None: none), checked: `shape` with the vectors contiguous."""
     if t is None:
         return _NO_VIEW
-    return View(t.data_ptr() or None, _stride(t, token), _stride(t, head), 0 if seq is None else _stride(t, seq))
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {list(shape)}; got {t.dtype} {list(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and t.numel():
+        raise ValueError(f"{name}'s head vectors must be contiguous")
+    d = shape[-1]  # stands in for the stride of a dimension of one, which addresses nothing
+    return View(t.data_ptr(), st[token] if shape[token] > 1 else d, st[head] if shape[head] > 1 else d,
+                0 if seq < 0 else st[seq] if shape[seq] > 1 else d)
 
 
-def _check_rows(name: str, t: torch.Tensor, shape, dtype, what: str):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or (t.numel() and t.stride(-1) != 1):
-        raise ValueError(f"{name} must be {what} of shape {list(shape)} with contiguous head vectors; got "
-                         f"{t.dtype} {list(t.shape)}")
-
-
-def _check_norm_rope(q, k, v, wq, wk, cos, sin):
-    """Checks of the token-major side that both directions share. Returns (N, Hq, Hk, d)."""
+def _norm_rope_sizes(q, k, wq, wk, cos, sin):
+    """Checks of what both directions share. Returns (N, Hq, Hk, d)."""
     if q.dim() != 3 or q.dtype not in _X_DTYPES:
         raise ValueError("q must be a bf16 or fp32 CUDA tensor [N, heads, d]")
     n, hq, d = q.shape
-    if v is not None and k is None:
-        raise ValueError("v comes with k")
-    hk = k.shape[1] if k is not None and k.dim() == 3 else 0
-    for name, t, h in (("q", q, hq), ("k", k, hk), ("v", v, hk)):
-        if t is not None:
-            _check_rows(name, t, (n, h, d), q.dtype, "a tensor of q's type")
+    hk = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be [N, heads, d]")
+        hk = k.shape[1]
     for name, t, shape in (("wq", wq, (d,)), ("wk", wk, (d,)), ("cos", cos, (n, d // 2)), ("sin", sin, (n, d // 2))):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {list(shape)}")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    _check_same_device(q.device, q=q, k=k, v=v, wq=wq, wk=wk, cos=cos, sin=sin)
     return n, hq, hk, d
 
 
@@ -527,40 +535,39 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[
     kv_rows they may also be a cache [N, Hk, rows, d] that takes one token of each of N sequences.
     A negative kv_rows[n] leaves token n out; one past the rows does too and is reported by
     device_status()."""
-    n, hq, hk, d = _check_norm_rope(q, k, v, wq, wk, cos, sin)
-    if kv_rows is not None and (kv_rows.dtype != torch.int32 or tuple(kv_rows.shape) != (n,)
-                                or not kv_rows.is_contiguous()):
-        raise ValueError("kv_rows must be a contiguous int32 tensor [N]")
-    if kv_rows is not None and (kv_offset or (k is not None and k_out is None) or (v is not None and v_out is None)):
-        raise ValueError("kv_rows needs k_out (and v_out) and takes no kv_offset")
-    for t, o in (("k", k_out), ("v", v_out)):
-        if o is not None and (k if t == "k" else v) is None:
-            raise ValueError(f"{t}_out without {t}")
+    n, hq, hk, d = _norm_rope_sizes(q, k, wq, wk, cos, sin)
     kv_offset = int(kv_offset)
+    if v is not None and k is None:
+        raise ValueError("v comes with k")
+    if (k_out is not None and k is None) or (v_out is not None and v is None):
+        raise ValueError("k_out comes with k, and v_out with v")
     if kv_offset < 0:
         raise ValueError("kv_offset must not be negative")
-    with _launch(q.device, stream) as st:
-        bf16 = torch.bfloat16
+    if kv_rows is not None:
+        if kv_rows.dtype != torch.int32 or kv_rows.shape != (n,) or not kv_rows.is_contiguous():
+            raise ValueError("kv_rows must be a contiguous int32 tensor [N]")
+        if kv_offset or (k is not None and k_out is None) or (v is not None and v_out is None):
+            raise ValueError("kv_rows needs k_out (and v_out) and takes no kv_offset")
+    device, x_dtype, bf16 = q.device, q.dtype, torch.bfloat16
+    qv, kv = _view("q", q, (n, hq, d), x_dtype, 0, 1), _view("k", k, (n, hk, d), x_dtype, 0, 1)
+    vv = _view("v", v, (n, hk, d), x_dtype, 0, 1)
+    _check_device(device, k, v, wq, wk, cos, sin, q_out, k_out, v_out, kv_rows)
+    with _launch(device, stream) as st:
         if q_out is None:
-            q_out = torch.empty(hq, n, d, dtype=bf16, device=q.device)
+            q_out = torch.empty((hq, n, d), dtype=bf16, device=device)
         if k is not None and k_out is None:
-            k_out = torch.empty(hk, kv_offset + n, d, dtype=bf16, device=q.device)
-        if v is not None and v_out is None:
-            v_out = torch.empty(hk, kv_offset + n, d, dtype=bf16, device=q.device)
-        _check_rows("q_out", q_out, (hq, n, d), bf16, "a bf16 tensor")
-        rows, dims = 0, 3
+            k_out = torch.empty((hk, kv_offset + n, d), dtype=bf16, device=device)
+        rows, kv_shape, dims = 0, None, (1, 0)
         if k_out is not None:
-            dims, rows = k_out.dim(), k_out.shape[-2]
-            lead = (n, hk) if kv_rows is not None and dims == 4 else (hk,)
-            _check_rows("k_out", k_out, (*lead, rows, d), bf16, "a bf16 tensor")
-            if v_out is not None:
-                _check_rows("v_out", v_out, k_out.shape, bf16, "a bf16 tensor")
-        _check_same_device(q.device, q_out=q_out, k_out=k_out, v_out=v_out, kv_rows=kv_rows)
-        kv_dims = (2, 1, 0) if dims == 4 else (1, 0)
+            rows, kv_shape = k_out.shape[-2], (hk, k_out.shape[-2], d)
+            if kv_rows is not None and k_out.dim() == 4:
+                kv_shape, dims = (n, *kv_shape), (2, 1, 0)
+        if v is not None and v_out is None:
+            v_out = torch.empty((hk, kv_offset + n, d) if kv_shape is None else kv_shape, dtype=bf16, device=device)
         _check(load().sparstar_qk_norm_rope(
-            _view(q, 0, 1), _view(k, 0, 1), _view(v, 0, 1), _X_DTYPES[q.dtype], n, hq, hk, d, _ptr(wq), _ptr(wk),
-            _ptr(cos), _ptr(sin), eps, int(interleaved), _view(q_out, 1, 0), _view(k_out, *kv_dims),
-            _view(v_out, *kv_dims), _ptr(kv_rows), kv_offset, rows, st), "sparstar_qk_norm_rope")
+            qv, kv, vv, _X_DTYPES[x_dtype], n, hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, interleaved,
+            _view("q_out", q_out, (hq, n, d), bf16, 1, 0), _view("k_out", k_out, kv_shape, bf16, *dims),
+            _view("v_out", v_out, kv_shape, bf16, *dims), _ptr(kv_rows), kv_offset, rows, st), "sparstar_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -575,41 +582,46 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tens
     Returns (dq_in, dk_in, dv_in, dwq, dwk): token-major in q's type (given outputs may be slices
     of one fused gradient) and fp32 [d] sums, dwq and dwk also where the weights were left out.
     The same inputs give the same bits."""
-    n, hq, hk, d = _check_norm_rope(q, k, None, wq, wk, cos, sin)
+    n, hq, hk, d = _norm_rope_sizes(q, k, wq, wk, cos, sin)
+    kv_offset = int(kv_offset)
     if (dk is None) != (k is None) or (dv is not None and k is None):
         raise ValueError("dk comes with k, and dv with both")
-    kv_offset = int(kv_offset)
-    _check_rows("dq", dq, (hq, n, d), torch.bfloat16, "a bf16 tensor")
+    if (dk_in is not None and dk is None) or (dv_in is not None and dv is None):
+        raise ValueError("dk_in comes with dk, and dv_in with dv")
+    device, x_dtype, bf16 = q.device, q.dtype, torch.bfloat16
+    views = [_view("dq", dq, (hq, n, d), bf16, 1, 0)]
     for name, t in (("dk", dk), ("dv", dv)):
-        if t is not None:
-            rows = t.shape[1] if t.dim() == 3 else 0
-            _check_rows(name, t, (hk, rows, d), torch.bfloat16, "a bf16 tensor")
-            if kv_offset < 0 or kv_offset + n > rows:
-                raise ValueError(f"{name} has no rows {kv_offset} to {kv_offset + n}")
-    with _launch(q.device, stream) as st:
+        rows = t.shape[1] if t is not None and t.dim() == 3 else 0
+        views.append(_view(name, t, (hk, rows, d), bf16, 1, 0))
+        if t is not None and (kv_offset < 0 or kv_offset + n > rows):
+            raise ValueError(f"{name} has no rows {kv_offset} to {kv_offset + n}")
+    views += [_view("q", q, (n, hq, d), x_dtype, 0, 1), _view("k", k, (n, hk, d), x_dtype, 0, 1)]
+    _check_device(device, dq, dk, dv, k, wq, wk, cos, sin, dq_in, dk_in, dv_in)
+    with _launch(device, stream) as st:
         if dq_in is None:
-            dq_in = torch.empty(n, hq, d, dtype=q.dtype, device=q.device)
+            dq_in = torch.empty((n, hq, d), dtype=x_dtype, device=device)
         if dk is not None and dk_in is None:
-            dk_in = torch.empty(n, hk, d, dtype=q.dtype, device=q.device)
+            dk_in = torch.empty((n, hk, d), dtype=x_dtype, device=device)
         if dv is not None and dv_in is None:
-            dv_in = torch.empty(n, hk, d, dtype=q.dtype, device=q.device)
-        for name, t, src, h in (("dq_in", dq_in, dq, hq), ("dk_in", dk_in, dk, hk), ("dv_in", dv_in, dv, hk)):
-            if t is not None:
-                if src is None:
-                    raise ValueError(f"{name} without its gradient")
-                _check_rows(name, t, (n, h, d), q.dtype, "a tensor of q's type")
-        _check_same_device(q.device, dq=dq, dk=dk, dv=dv, dq_in=dq_in, dk_in=dk_in, dv_in=dv_in)
-        dw = torch.empty(2, d, dtype=torch.float32, device=q.device)
-        nbytes = ctypes.c_size_t()
-        _check(load().sparstar_qk_norm_rope_bwd_workspace_size(d, ctypes.byref(nbytes)),
-               "sparstar_qk_norm_rope_bwd_workspace_size")
-        ws = torch.empty(nbytes.value, dtype=torch.uint8, device=q.device)
+            dv_in = torch.empty((n, hk, d), dtype=x_dtype, device=device)
+        dw = torch.empty((2, d), dtype=torch.float32, device=device)
+        nbytes = _norm_rope_bwd_workspace_size(d)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        at = dw.data_ptr()
         _check(load().sparstar_qk_norm_rope_bwd(
-            _view(dq, 1, 0), _view(dk, 1, 0), _view(dv, 1, 0), _view(q, 0, 1), _view(k, 0, 1), _X_DTYPES[q.dtype], n,
-            hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, int(interleaved), kv_offset, _view(dq_in, 0, 1),
-            _view(dk_in, 0, 1), _view(dv_in, 0, 1), _ptr(dw[0]), _ptr(dw[1]) if dk is not None else None, _ptr(ws),
-            nbytes.value, st), "sparstar_qk_norm_rope_bwd")
+            *views, _X_DTYPES[x_dtype], n, hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, interleaved,
+            kv_offset, _view("dq_in", dq_in, (n, hq, d), x_dtype, 0, 1),
+            _view("dk_in", dk_in, (n, hk, d), x_dtype, 0, 1), _view("dv_in", dv_in, (n, hk, d), x_dtype, 0, 1), at,
+            at + 4 * d if dk is not None else None, ws.data_ptr(), nbytes, st), "sparstar_qk_norm_rope_bwd")
     return dq_in, dk_in, dv_in, dw[0], dw[1] if dk is not None else None
+
+
+@functools.lru_cache(maxsize=None)
+def _norm_rope_bwd_workspace_size(head_dim: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().sparstar_qk_norm_rope_bwd_workspace_size(head_dim, ctypes.byref(out)),
+           "sparstar_qk_norm_rope_bwd_workspace_size")
+    return int(out.value)
 
 
 # ------------------------------------------------------------------ one query token per sequence
@@ -626,7 +638,7 @@ def _check_cache(k, v, kv_len, means, q=None):
     _check_kv_len(kv_len, b)
     if q is not None:
         _check_token_q(q, b, hk, d)
-    _check_same_device(k.device, k=k, v=v, kv_len=kv_len, means=means, q=q)
+    _check_device(k.device, k, v, kv_len, means, q)
     return b, hk, s, d
 
 
@@ -689,7 +701,7 @@ def token_select(q: torch.Tensor, means: torch.Tensor, kv_len: torch.Tensor, kee
     _check_kv_len(kv_len, b)
     _check_token_q(q, b, hk, d)
     _check_lists(idx, cnt, b, hk, keep)
-    _check_same_device(q.device, means=means, kv_len=kv_len, idx=idx, cnt=cnt)
+    _check_device(q.device, means, kv_len, idx, cnt)
     with _launch(q.device, stream) as st:
         idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
         cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt
@@ -710,7 +722,7 @@ def token_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.
         raise ValueError("idx must be contiguous int32 [B, Hk, keep]")
     _check_lists(idx, cnt, b, hk, idx.shape[2])
     _check_token_out(o, lse, q)
-    _check_same_device(q.device, idx=idx, cnt=cnt, o=o, lse=lse)
+    _check_device(q.device, idx, cnt, o, lse)
     with _launch(q.device, stream) as st:
         o = torch.empty_like(q) if o is None else o
         if want_lse and lse is None:
@@ -730,7 +742,7 @@ def token_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: tor
     keep = int(keep)
     _check_lists(idx, cnt, b, hk, keep)
     _check_token_out(o, lse, q)
-    _check_same_device(q.device, idx=idx, cnt=cnt, o=o, lse=lse)
+    _check_device(q.device, idx, cnt, o, lse)
     with _launch(q.device, stream) as st:
         idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
         cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt

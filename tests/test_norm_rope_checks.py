@@ -68,6 +68,8 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         S.qk_norm_rope(q, k)
     with pytest.raises(ValueError, match="k must be"):
         S.qk_norm_rope(q, k[:3])
+    with pytest.raises(ValueError, match="contiguous"):
+        S.qk_norm_rope(q.repeat(1, 1, 2)[..., ::2], k)
     with pytest.raises(ValueError, match="q must be"):
         S.qk_norm_rope(q.half(), k)
     with pytest.raises(ValueError, match="come together"):
