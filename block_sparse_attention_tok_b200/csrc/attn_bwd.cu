@@ -145,8 +145,8 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   p.cnt = cnt;
   p.col_row = col_row;
   p.col_at = col_at;
-  p.lse2 = lse2;
-  p.delta = delta;
+  p.neg_lse2 = lse2;
+  p.neg_delta = delta;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);

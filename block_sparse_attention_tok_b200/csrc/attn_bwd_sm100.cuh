@@ -62,8 +62,8 @@ struct BwdParams {
   const int32_t* cnt;      // [H, nqb]
   const int32_t* col_row;  // [H, nqb * kmax] query blocks of each KV block (dkv)
   const int32_t* col_at;   // [H, nkb + 1] first entry of each KV block in col_row
-  const float* lse2;       // [H, nqb * B] lse * log2(e), +inf past n_q
-  const float* delta;      // [H, nqb * B], 0 past n_q
+  const float* neg_lse2;   // [H, nqb * B] -lse log2(e), -inf past n_q
+  const float* neg_delta;  // [H, nqb * B] -delta, 0 past n_q
   __nv_bfloat16 *dq, *dk, *dv;
   unsigned* status;
   int* next;               // item counter, 0 at launch
@@ -96,7 +96,10 @@ struct BwdPhaseBars {
   uint64_t held_full, held_empty;    // the held pair of tiles (K, V)
   uint64_t s_full[2], p_full;        // S ready / P written
   uint64_t dp_full, dp_read;         // dP ready / dP taken into registers (dQ only)
-  uint64_t ds_full, acc_full;
+  // dS written. dQ uses both in turn: a warp may reach tile n + 1 (whose S and dP wait only for
+  // dP(n) to be read) before another has arrived for tile n, and must not be counted there.
+  uint64_t ds_full[2];
+  uint64_t acc_full;
 };
 
 struct BwdBars {
@@ -121,13 +124,13 @@ __device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
       mbar_init(&b->st_full[i], 1);
       mbar_init(&b->st_empty[i], 1);
       mbar_init(&b->s_full[i], 1);
+      mbar_init(&b->ds_full[i], 256);
     }
     mbar_init(&b->held_full, 1);
     mbar_init(&b->held_empty, 1);
     mbar_init(&b->p_full, 256);
     mbar_init(&b->dp_full, 1);
     mbar_init(&b->dp_read, 256);
-    mbar_init(&b->ds_full, 256);
     mbar_init(&b->acc_full, 1);
   }
   for (int i = 0; i < 2; ++i) {
@@ -160,12 +163,23 @@ __device__ __forceinline__ void bwd_drain_ring(uint64_t* full, uint32_t stages, 
 // its partner still reads.
 __device__ __forceinline__ uint32_t bwd_a_col(int kk) { return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8); }
 
-// 64 fp32 values -> bf16 pairs -> 32 TMEM columns.
-__device__ __forceinline__ void bwd_store_half(uint32_t taddr, const float (&x)[64]) {
+// 64 fp32 values (as pairs of neighbours) -> bf16 pairs -> 32 TMEM columns.
+__device__ __forceinline__ void bwd_store_half(uint32_t taddr, const float2 (&x)[32]) {
   uint32_t pk[32];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+  for (int e = 0; e < 32; ++e) pk[e] = pack_bf16x2(x[e].x, x[e].y);
   tmem_st32(taddr, pk);
+}
+
+// Columns 2e and 2e + 1 of half a row.
+__device__ __forceinline__ float2 bwd_pair(const uint32_t (&r)[2][32], int e) {
+  return make_float2(__uint_as_float(r[e >> 4][(2 * e) & 31]), __uint_as_float(r[e >> 4][(2 * e + 1) & 31]));
+}
+
+// P of a pair of columns: exp2(s * scale - lse2).
+__device__ __forceinline__ float2 bwd_exp(float2 s, float2 scale, float2 neg_lse) {
+  const float2 x = __ffma2_rn(s, scale, neg_lse);
+  return make_float2(ex2_approx(x.x), ex2_approx(x.y));
 }
 
 __device__ __forceinline__ void bwd_load_half(uint32_t taddr, uint32_t (&r)[2][32]) {
@@ -340,8 +354,8 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
 #pragma unroll
               for (int b = 0; b < BPT; ++b) {
                 const int64_t at = (static_cast<int64_t>(h) * p.nqb + qb[b]) * B;
-                bulk_load(st + b * B * 4, p.lse2 + at, B * 4, &bk->st_full[sb]);
-                bulk_load(st + 512 + b * B * 4, p.delta + at, B * 4, &bk->st_full[sb]);
+                bulk_load(st + b * B * 4, p.neg_lse2 + at, B * 4, &bk->st_full[sb]);
+                bulk_load(st + 512 + b * B * 4, p.neg_delta + at, B * 4, &bk->st_full[sb]);
               }
               if (!(ok = mbar_wait(&bk->a_empty[sa], ((tk / C::kStagesA) & 1u) ^ 1u, abort_flag, p.status))) {
                 bwd_drain(&bk->st_full[sb], (tk / 2) & 1u);
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
             }
             __syncwarp();
             if (!last && !(ok = k_issue_s(tk + 1))) break;
-            if (!(ok = wait_all(&bk->ds_full, tk & 1u))) break;
+            if (!(ok = wait_all(&bk->ds_full[0], tk & 1u))) break;
             tc_fence_after();
             if (elect_one()) {
               gather(tmem + kDK, tmem + kDPk, ra_mn + stage_of(sa), n > 0);
@@ -506,7 +520,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           for (int n = 0; ok && n < n_tiles; ++n, ++tq) {
             const bool last = n == n_tiles - 1;
             if (!last && !(ok = q_issue_s(tq + 1) && q_issue_dp(tq + 1, n == n_tiles - 2))) break;
-            if (!(ok = wait_all(&bq->ds_full, tq & 1u))) break;
+            if (!(ok = wait_all(&bq->ds_full[tq & 1u], (tq >> 1) & 1u))) break;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t sa = tq % C::kStagesA;
@@ -533,6 +547,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
     // in their rows of P and dS only reaches accumulator rows that are never stored.
     const bool idle = B < 128 && wq * 32 >= B;
     const bool ragged_kv = p.n_kv % B != 0;
+    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t tk = 0, tq = 0, dk_done = 0, dq_done = 0;
     bool ok = true, in_dq = false;
     for (uint32_t k = 0; ok; ++k) {
@@ -559,26 +574,22 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (idle) {
             mbar_arrive(&bk->p_full);
             if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
-            mbar_arrive(&bk->ds_full);
+            mbar_arrive(&bk->ds_full[0]);
             continue;
           }
           tc_fence_after();
           uint32_t r[2][32];
-          float pr[64];
+          float2 pr[32];
           bwd_load_half(t_s, r);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float4 l = lse[e];
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = 4 * e + i;
-              pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, -lv[i]));
-            }
+            pr[2 * e] = bwd_exp(bwd_pair(r, 2 * e), scale2, make_float2(l.x, l.y));
+            pr[2 * e + 1] = bwd_exp(bwd_pair(r, 2 * e + 1), scale2, make_float2(l.z, l.w));
           }
           if (BPT > 1 && half == 1 && 2 * n + 1 >= n_ent) {  // odd last entry: its half repeats a block
 #pragma unroll
-            for (int c = 0; c < 64; ++c) pr[c] = 0.f;
+            for (int e = 0; e < 32; ++e) pr[e] = make_float2(0.f, 0.f);
           }
           bwd_store_half(t_s, pr);
           tmem_wait_st();
@@ -590,17 +601,13 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float4 l = del[e];
-            const float lv[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = 4 * e + i;
-              pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - lv[i];
-            }
+            pr[2 * e] = __fmul2_rn(pr[2 * e], __fadd2_rn(bwd_pair(r, 2 * e), make_float2(l.x, l.y)));
+            pr[2 * e + 1] = __fmul2_rn(pr[2 * e + 1], __fadd2_rn(bwd_pair(r, 2 * e + 1), make_float2(l.z, l.w)));
           }
           bwd_store_half(t_dp, pr);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&bk->ds_full);
+          mbar_arrive(&bk->ds_full[0]);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bk->acc_full, dk_done & 1u))) break;
@@ -617,11 +624,11 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         }
         const int32_t* list = p.idx + static_cast<int64_t>(iq) * p.kmax;
         const int64_t tok = static_cast<int64_t>(blk) * B + row;
-        float neg_lse = 0.f, delta = 0.f;
+        float2 neg_lse = make_float2(0.f, 0.f), neg_delta = make_float2(0.f, 0.f);
         if (row < B) {
           const int64_t at = static_cast<int64_t>(iq) * B + row;
-          neg_lse = -__ldg(p.lse2 + at);
-          delta = __ldg(p.delta + at);
+          neg_lse.x = neg_lse.y = __ldg(p.neg_lse2 + at);
+          neg_delta.x = neg_delta.y = __ldg(p.neg_delta + at);
         }
         for (int n = 0; n < n_tiles; ++n, ++tq) {
           const uint32_t t_s = tmem + lane_off + kS + 128u * (tq & 1u) + 64 * half;
@@ -640,20 +647,21 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (idle) {
             if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
             mbar_arrive(&bq->dp_read);
-            mbar_arrive(&bq->ds_full);
+            mbar_arrive(&bq->ds_full[tq & 1u]);
             continue;
           }
           tc_fence_after();
           uint32_t r[2][32];
-          float pr[64];
+          float2 pr[32];
           bwd_load_half(t_s, r);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            pr[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), p.scale_log2, neg_lse));
+          for (int e = 0; e < 32; ++e) pr[e] = bwd_exp(bwd_pair(r, e), scale2, neg_lse);
           if (nv < 64) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c >= nv) pr[c] = 0.f;
+            for (int e = 0; e < 32; ++e) {
+              if (2 * e >= nv) pr[e].x = 0.f;
+              if (2 * e + 1 >= nv) pr[e].y = 0.f;
+            }
           }
           if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
           tc_fence_after();
@@ -661,11 +669,11 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(&bq->dp_read);
 #pragma unroll
-          for (int c = 0; c < 64; ++c) pr[c] *= __uint_as_float(r[c >> 5][c & 31]) - delta;
+          for (int e = 0; e < 32; ++e) pr[e] = __fmul2_rn(pr[e], __fadd2_rn(bwd_pair(r, e), neg_delta));
           bwd_store_half(t_s, pr);
           tmem_wait_st();
           tc_fence_before();
-          mbar_arrive(&bq->ds_full);
+          mbar_arrive(&bq->ds_full[tq & 1u]);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bq->acc_full, dq_done & 1u))) break;
@@ -690,14 +698,14 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
 
 // ------------------------------------------------------------------------ row statistics
 //
-// lse2 = lse log2(e) and delta = do . o of every query row, padded to whole blocks (+inf and 0
-// past n_q: such a row's P is 0), so that a block's statistics are one aligned copy. One read of
-// o and do, D / 8 lanes a row. Memory-bound and small beside the products.
+// -lse log2(e) and -delta = -do . o of every query row, padded to whole blocks (-inf and 0 past
+// n_q: such a row's P is 0), so that a block's statistics are one aligned copy. One read of o and
+// do, D / 8 lanes a row. Memory-bound and small beside the products.
 template <int D>
 __global__ void __launch_bounds__(256)
     bwd_rows_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ d_o,
-                    const float* __restrict__ lse, int64_t n_q, int64_t n_pad, float* __restrict__ lse2,
-                    float* __restrict__ delta, int* __restrict__ next) {
+                    const float* __restrict__ lse, int64_t n_q, int64_t n_pad, float* __restrict__ neg_lse2,
+                    float* __restrict__ neg_delta, int* __restrict__ next) {
   constexpr int G = D / 8;
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *next = 0;  // the item counter of this call
   const int l = threadIdx.x % G;
@@ -718,8 +726,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
   if (l == 0 && row < n_pad) {
-    lse2[h * n_pad + row] = row < n_q ? __ldg(lse + h * n_q + row) * 1.4426950408889634f : INFINITY;
-    delta[h * n_pad + row] = s;
+    neg_lse2[h * n_pad + row] = row < n_q ? __ldg(lse + h * n_q + row) * -1.4426950408889634f : -INFINITY;
+    neg_delta[h * n_pad + row] = -s;
   }
 }
 

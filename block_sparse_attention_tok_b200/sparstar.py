@@ -613,7 +613,8 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tens
             kv_offset, _view("dq_in", dq_in, (n, hq, d), x_dtype, 0, 1),
             _view("dk_in", dk_in, (n, hk, d), x_dtype, 0, 1), _view("dv_in", dv_in, (n, hk, d), x_dtype, 0, 1), at,
             at + 4 * d if dk is not None else None, ws.data_ptr(), nbytes, st), "sparstar_qk_norm_rope_bwd")
-    return dq_in, dk_in, dv_in, dw[0], dw[1] if dk is not None else None
+    dwq, dwk = dw.unbind(0)
+    return dq_in, dk_in, dv_in, dwq, dwk if dk is not None else None
 
 
 @functools.lru_cache(maxsize=None)
