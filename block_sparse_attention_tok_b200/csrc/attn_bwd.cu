@@ -35,7 +35,7 @@ int set_kernel_attrs(const DeviceInfo* dev) {
   if ((rc = set_attrs<128, 128>()) != SPARSTAR_OK || (rc = set_attrs<64, 128>()) != SPARSTAR_OK ||
       (rc = set_attrs<128, 64>()) != SPARSTAR_OK || (rc = set_attrs<64, 64>()) != SPARSTAR_OK)
     return rc;
-  for (auto kernel : {reinterpret_cast<const void*>(mask_count_kernel), reinterpret_cast<const void*>(mask_fill_kernel)})
+  for (auto kernel : {bwd_prep_kernel<128>, bwd_prep_kernel<64>})
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaskMaxBlocks * 4) != cudaSuccess)
       return SPARSTAR_ERR_CUDA;
   g_attrs_set[dev->index] = true;
@@ -43,7 +43,7 @@ int set_kernel_attrs(const DeviceInfo* dev) {
 }
 
 struct BwdWorkspace {
-  size_t next, lse2, delta, chunk_cnt, col_at, col_row, total;
+  size_t next, lse2, delta, words, place, twice, col_at, col_row, total;
 };
 
 BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t kmax) {
@@ -53,8 +53,11 @@ BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t 
   w.next = 0;
   w.lse2 = 256;
   w.delta = w.lse2 + rows;
-  w.chunk_cnt = w.delta + rows;
-  w.col_at = w.chunk_cnt + align256(h * ((nqb + kMaskRows - 1) / kMaskRows) * nkb * 4);
+  const size_t chunks = static_cast<size_t>((nqb + kMaskRows - 1) / kMaskRows);
+  w.words = w.delta + rows;
+  w.place = w.words + align256(h * chunks * nkb * 4);
+  w.twice = w.place + align256(h * chunks * nkb * 4);
+  w.col_at = w.twice + align256(h * chunks * 4);
   w.col_row = w.col_at + align256(h * (nkb + 1) * 4);
   w.total = w.col_row + align256(h * nqb * kmax * 4);
   return w;
@@ -76,7 +79,8 @@ template <int D, int B>
 void launch_bwd(const BwdMaps& maps, const BwdParams& p, int sms, cudaStream_t st) {
   using C = BwdConfig<D, B>;
   const int items = p.n_dkv + p.n_dq;
-  attn_bwd_kernel<D, B><<<items < sms ? items : sms, C::kThreads, C::kSmemBytes, st>>>(maps, p);
+  launch_after(attn_bwd_kernel<D, B>, dim3(static_cast<unsigned>(items < sms ? items : sms)), dim3(C::kThreads),
+               C::kSmemBytes, st, maps, p);
 }
 
 }  // namespace
@@ -135,48 +139,60 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
       return rc;
   }
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  float* lse2 = reinterpret_cast<float*>(w + ws.lse2);
-  float* delta = reinterpret_cast<float*>(w + ws.delta);
-  int32_t* chunk_cnt = reinterpret_cast<int32_t*>(w + ws.chunk_cnt);
-  int32_t* col_at = reinterpret_cast<int32_t*>(w + ws.col_at);
-  int32_t* col_row = reinterpret_cast<int32_t*>(w + ws.col_row);
+  BwdPrep r = {};
+  r.o = static_cast<const __nv_bfloat16*>(o);
+  r.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  r.lse = lse;
+  r.idx = idx;
+  r.cnt = cnt;
+  r.neg_lse2 = reinterpret_cast<float*>(w + ws.lse2);
+  r.neg_delta = reinterpret_cast<float*>(w + ws.delta);
+  r.words = reinterpret_cast<uint32_t*>(w + ws.words);
+  r.place = reinterpret_cast<int32_t*>(w + ws.place);
+  r.twice = reinterpret_cast<int32_t*>(w + ws.twice);
+  r.col_at = reinterpret_cast<int32_t*>(w + ws.col_at);
+  r.col_row = reinterpret_cast<int32_t*>(w + ws.col_row);
+  r.next = reinterpret_cast<int*>(w + ws.next);
+  r.status = dev->status;
+  r.n_q = n_q;
+  r.n_pad = nqb * block;
+  r.heads = heads;
+  r.nqb = static_cast<int>(nqb);
+  r.nkb = static_cast<int>(nkb);
+  r.kmax = kmax;
+  r.n_chunks = static_cast<int>((nqb + kMaskRows - 1) / kMaskRows);
   BwdParams p = {};
   p.idx = idx;
   p.cnt = cnt;
-  p.col_row = col_row;
-  p.col_at = col_at;
-  p.neg_lse2 = lse2;
-  p.neg_delta = delta;
+  p.col_row = r.col_row;
+  p.col_at = r.col_at;
+  p.neg_lse2 = r.neg_lse2;
+  p.neg_delta = r.neg_delta;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.status = dev->status;
-  p.next = reinterpret_cast<int*>(w + ws.next);
+  p.next = r.next;
   p.n_q = n_q;
   p.n_kv = n_kv;
-  p.nqb = static_cast<int>(nqb);
-  p.nkb = static_cast<int>(nkb);
+  p.nqb = r.nqb;
+  p.nkb = r.nkb;
   p.kmax = kmax;
   p.n_dkv = static_cast<int>(heads * nkb);
   p.n_dq = static_cast<int>(heads * nqb);
   p.scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   p.scale_log2 = p.scale * 1.4426950408889634f;
 
-  const int64_t n_pad = nqb * block;
   const int rows_per_cta = 256 / (head_dim / 8);
-  const dim3 rows_grid(static_cast<unsigned>((n_pad + rows_per_cta - 1) / rows_per_cta), static_cast<unsigned>(heads));
-  const auto* o16 = static_cast<const __nv_bfloat16*>(o);
-  const auto* do16 = static_cast<const __nv_bfloat16*>(d_o);
+  const int64_t row_tiles = (r.n_pad + rows_per_cta - 1) / rows_per_cta * heads;
+  const int64_t row_ctas = row_tiles < 16 * dev->sms ? row_tiles : 16 * dev->sms;
+  const unsigned prep_grid = static_cast<unsigned>(static_cast<int64_t>(r.n_chunks) * heads + row_ctas);
+  const size_t word_bytes = static_cast<size_t>(nkb) * 4;
   if (head_dim == 128)
-    bwd_rows_kernel<128><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta, p.next);
+    bwd_prep_kernel<128><<<prep_grid, 256, word_bytes, st>>>(r);
   else
-    bwd_rows_kernel<64><<<rows_grid, 256, 0, st>>>(o16, do16, lse, n_q, n_pad, lse2, delta, p.next);
-  const int n_chunks = (p.nqb + kMaskRows - 1) / kMaskRows;
-  const dim3 mask_grid(static_cast<unsigned>(n_chunks), static_cast<unsigned>(heads));
-  const size_t counters = static_cast<size_t>(nkb) * 4;
-  mask_count_kernel<<<mask_grid, 256, counters, st>>>(idx, cnt, p.nqb, p.nkb, kmax, chunk_cnt, dev->status);
-  mask_scan_kernel<<<heads, 1024, 0, st>>>(p.nkb, n_chunks, chunk_cnt, col_at);
-  mask_fill_kernel<<<mask_grid, 256, counters, st>>>(idx, cnt, p.nqb, p.nkb, kmax, chunk_cnt, col_at, col_row);
+    bwd_prep_kernel<64><<<prep_grid, 256, word_bytes, st>>>(r);
+  launch_after(bwd_lists_kernel, dim3(static_cast<unsigned>(heads)), dim3(1024), 0, st, r);
   if (head_dim == 128) {
     if (block == 128)
       launch_bwd<128, 128>(maps, p, dev->sms, st);

@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
+  griddep_wait();  // row statistics, lists and the item counter come from the kernels before
   constexpr uint32_t kS = 0, kDPk = 128, kDV = 256, kDK = 384;  // dK, dV items
   constexpr uint32_t kDPq = 256, kDQ = 384;                     // dQ items
 
@@ -696,92 +697,152 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
   }
 }
 
-// ------------------------------------------------------------------------ row statistics
+// ------------------------------------------------------------------------ preparation
 //
-// -lse log2(e) and -delta = -do . o of every query row, padded to whole blocks (-inf and 0 past
-// n_q: such a row's P is 0), so that a block's statistics are one aligned copy. One read of o and
-// do, D / 8 lanes a row. Memory-bound and small beside the products.
-template <int D>
-__global__ void __launch_bounds__(256)
-    bwd_rows_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ d_o,
-                    const float* __restrict__ lse, int64_t n_q, int64_t n_pad, float* __restrict__ neg_lse2,
-                    float* __restrict__ neg_delta, int* __restrict__ next) {
-  constexpr int G = D / 8;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *next = 0;  // the item counter of this call
-  const int l = threadIdx.x % G;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / G) + threadIdx.x / G;
-  const int64_t h = blockIdx.y;
-  float s = 0.f;
-  if (row < n_q) {
-    const int64_t at = (h * n_q + row) * D + 8 * l;
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(o + at));
-    const uint4 b = __ldcs(reinterpret_cast<const uint4*>(d_o + at));
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
-      s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
-    }
-  }
-#pragma unroll
-  for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-  if (l == 0 && row < n_pad) {
-    neg_lse2[h * n_pad + row] = row < n_q ? __ldg(lse + h * n_q + row) * -1.4426950408889634f : -INFINITY;
-    neg_delta[h * n_pad + row] = -s;
-  }
-}
-
-// ------------------------------------------------------------------------ transposed lists
-//
-// Query blocks of each KV block, ascending, from the kept lists: a counting sort that is stable
-// by rows. Rows are cut into chunks of kMaskRows; each (chunk, head) counts its entries per KV
-// block, the counts are scanned over chunks and blocks, and each (chunk, head) places its rows
-// one after another. A block listed twice in a row is placed twice (the forward pass attends to
-// it twice). Out-of-range entries are clamped as the forward pass clamps them, and recorded.
+// bwd_prep_kernel, in one launch:
+//   rows: -lse log2(e) and -delta = -do . o of every query row, padded to whole blocks (-inf and 0
+//   past n_q: such a row's P is 0), so that a block's statistics are one aligned copy. One read of
+//   o and do, D / 8 lanes a row; memory-bound.
+//   masks: for each (chunk of 32 query-block rows, head), one word per KV block with the rows that
+//   keep it. A row that lists a block twice is noted in `twice`.
+// bwd_lists_kernel, one CTA per head: the query blocks of each KV block, ascending. Word counts are
+// scanned over chunks and blocks, then every word places its rows. In a chunk with a block listed
+// twice the counts come from the lists themselves (the forward pass attends to it twice, so it is
+// placed twice). Out-of-range entries are clamped as the forward pass clamps them, and recorded.
 constexpr int kMaskRows = 32;
-constexpr int kMaskMaxBlocks = 49152;  // KV blocks at most: one 4-byte counter each in shared memory
+constexpr int kMaskMaxBlocks = 49152;  // KV blocks at most: one 4-byte word each in shared memory
 
-__global__ void __launch_bounds__(256)
-    mask_count_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt, int nqb, int nkb, int kmax,
-                      int32_t* __restrict__ chunk_cnt, unsigned* status) {
-  extern __shared__ int32_t hist[];
-  const int chunk = blockIdx.x, h = blockIdx.y;
-  for (int j = threadIdx.x; j < nkb; j += blockDim.x) hist[j] = 0;
-  __syncthreads();
-  const int r1 = min(nqb, (chunk + 1) * kMaskRows);
-  for (int i = chunk * kMaskRows; i < r1; ++i) {
-    const int64_t at = static_cast<int64_t>(h) * nqb + i;
-    const int c0 = __ldg(cnt + at), c = bwd_count(c0, kmax);
-    if (c != c0 && threadIdx.x == 0) atomicOr(status, kStatusBounds);
-    for (int e = threadIdx.x; e < c; e += blockDim.x) {
-      const int j0 = __ldg(idx + at * kmax + e), j = bwd_block(j0, nkb);
-      if (j != j0) atomicOr(status, kStatusBounds);
-      atomicAdd(&hist[j], 1);
+struct BwdPrep {
+  const __nv_bfloat16 *o, *d_o;
+  const float* lse;
+  const int32_t *idx, *cnt;
+  float *neg_lse2, *neg_delta;
+  uint32_t* words;   // [H, chunks, nkb]
+  int32_t* place;    // [H, chunks, nkb] first place of each word's rows within its KV block
+  int32_t* twice;    // [H, chunks]
+  int32_t *col_at, *col_row;
+  int* next;
+  unsigned* status;
+  int64_t n_q, n_pad;
+  int heads, nqb, nkb, kmax, n_chunks;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdPrep p) {
+  extern __shared__ uint32_t words[];
+  __shared__ int32_t counts[kMaskRows];
+  __shared__ int32_t twice;
+  griddep_launch_dependents();
+  const int n_mask = p.n_chunks * p.heads;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.next = 0;  // the item counter of this call
+  if (static_cast<int>(blockIdx.x) < n_mask) {
+    const int h = blockIdx.x / p.n_chunks, chunk = blockIdx.x - h * p.n_chunks;
+    const int64_t row0 = static_cast<int64_t>(h) * p.nqb + chunk * kMaskRows;
+    const int rows = min(kMaskRows, p.nqb - chunk * kMaskRows);
+    for (int j = threadIdx.x; j < p.nkb; j += 256) words[j] = 0u;
+    if (threadIdx.x < rows) {
+      const int c0 = __ldg(p.cnt + row0 + threadIdx.x), c = bwd_count(c0, p.kmax);
+      if (c != c0) atomicOr(p.status, kStatusBounds);
+      counts[threadIdx.x] = c;
+    }
+    if (threadIdx.x == 0) twice = 0;
+    __syncthreads();
+    // four entries in flight per thread
+    const uint32_t kmax = p.kmax, total = rows * kmax;  // at most nqb * kmax: 31 bits
+    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += 4 * 256) {
+      int j[4], r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t i = i0 + u * 256;
+        r[u] = i < total ? static_cast<int>(i / kmax) : -1;
+        if (r[u] >= 0 && static_cast<int>(i - r[u] * kmax) < counts[r[u]])
+          j[u] = __ldg(p.idx + row0 * p.kmax + i);
+        else
+          r[u] = -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (r[u] >= 0) {
+          const int jc = bwd_block(j[u], p.nkb);
+          if (jc != j[u]) atomicOr(p.status, kStatusBounds);
+          if ((atomicOr(&words[jc], 1u << r[u]) >> r[u]) & 1u) twice = 1;
+        }
+    }
+    __syncthreads();
+    uint32_t* out = p.words + static_cast<int64_t>(blockIdx.x) * p.nkb;
+    for (int j = threadIdx.x; j < p.nkb; j += 256) out[j] = words[j];
+    if (threadIdx.x == 0) p.twice[blockIdx.x] = twice;
+    return;
+  }
+  constexpr int G = D / 8, kRows = 256 / G;
+  const int l = threadIdx.x % G;
+  const int64_t tiles = (p.n_pad + kRows - 1) / kRows, all = tiles * p.heads;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) - n_mask; t < all; t += gridDim.x - n_mask) {
+    const int64_t h = t / tiles, row = (t - h * tiles) * kRows + threadIdx.x / G;
+    float s = 0.f;
+    if (row < p.n_q) {
+      const int64_t at = (h * p.n_q + row) * D + 8 * l;
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p.o + at));
+      const uint4 b = __ldcs(reinterpret_cast<const uint4*>(p.d_o + at));
+      const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+        s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+      }
+    }
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (l == 0 && row < p.n_pad) {
+      p.neg_lse2[h * p.n_pad + row] =
+          row < p.n_q ? __ldg(p.lse + h * p.n_q + row) * -1.4426950408889634f : -INFINITY;
+      p.neg_delta[h * p.n_pad + row] = -s;
     }
   }
-  __syncthreads();
-  int32_t* out = chunk_cnt + (static_cast<int64_t>(h) * gridDim.x + chunk) * nkb;
-  for (int j = threadIdx.x; j < nkb; j += blockDim.x) out[j] = hist[j];
 }
 
-// One CTA per head: chunk_cnt becomes each chunk's first place within a KV block, col_at the
-// block's first place within the head.
-__global__ void __launch_bounds__(1024)
-    mask_scan_kernel(int nkb, int n_chunks, int32_t* __restrict__ chunk_cnt, int32_t* __restrict__ col_at) {
+// How often the rows of a chunk list block j; with `out` each listing's row is written there.
+__device__ inline int bwd_scan_lists(const BwdPrep& p, int h, int chunk, int j, int32_t* out) {
+  const int r1 = min(p.nqb, (chunk + 1) * kMaskRows);
+  int n = 0;
+  for (int i = chunk * kMaskRows; i < r1; ++i) {
+    const int64_t row = static_cast<int64_t>(h) * p.nqb + i;
+    const int c = bwd_count(__ldg(p.cnt + row), p.kmax);
+    for (int e = 0; e < c; ++e)
+      if (bwd_block(__ldg(p.idx + row * p.kmax + e), p.nkb) == j) {
+        if (out != nullptr) out[n] = i;
+        ++n;
+      }
+  }
+  return n;
+}
+
+__global__ void __launch_bounds__(1024) bwd_lists_kernel(const BwdPrep p) {
   __shared__ int32_t warp_sum[32];
   __shared__ int32_t base;
+  griddep_launch_dependents();
+  griddep_wait();
   const int h = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int32_t* cc = chunk_cnt + static_cast<int64_t>(h) * n_chunks * nkb;
-  int32_t* at = col_at + static_cast<int64_t>(h) * (nkb + 1);
+  const uint32_t* words = p.words + static_cast<int64_t>(h) * p.n_chunks * p.nkb;
+  int32_t* place = p.place + static_cast<int64_t>(h) * p.n_chunks * p.nkb;
+  const int32_t* twice = p.twice + static_cast<int64_t>(h) * p.n_chunks;
+  int32_t* at = p.col_at + static_cast<int64_t>(h) * (p.nkb + 1);
+  int32_t* rows = p.col_row + static_cast<int64_t>(h) * p.nqb * p.kmax;
   if (threadIdx.x == 0) base = 0;
-  for (int j0 = 0; j0 < nkb; j0 += 1024) {
+  for (int j0 = 0; j0 < p.nkb; j0 += 1024) {
     const int j = j0 + threadIdx.x;
     int total = 0;
-    if (j < nkb)
-      for (int c = 0; c < n_chunks; ++c) {
-        const int v = cc[static_cast<int64_t>(c) * nkb + j];
-        cc[static_cast<int64_t>(c) * nkb + j] = total;
-        total += v;
+    if (j < p.nkb)
+      for (int c0 = 0; c0 < p.n_chunks; c0 += 8) {
+        uint32_t x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) x[u] = c0 + u < p.n_chunks ? words[static_cast<int64_t>(c0 + u) * p.nkb + j] : 0u;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (c0 + u < p.n_chunks) {
+            place[static_cast<int64_t>(c0 + u) * p.nkb + j] = total;
+            total += twice[c0 + u] ? bwd_scan_lists(p, h, c0 + u, j, nullptr) : __popc(x[u]);
+          }
       }
     int incl = total;
 #pragma unroll
@@ -802,31 +863,23 @@ __global__ void __launch_bounds__(1024)
     }
     __syncthreads();
     const int before = base + (w > 0 ? warp_sum[w - 1] : 0) + incl - total;
-    if (j < nkb) at[j] = before;
+    if (j < p.nkb) at[j] = before;
     __syncthreads();
     if (threadIdx.x == 1023) base = before + total;
     __syncthreads();
   }
-  if (threadIdx.x == 0) at[nkb] = base;
-}
-
-__global__ void __launch_bounds__(256)
-    mask_fill_kernel(const int32_t* __restrict__ idx, const int32_t* __restrict__ cnt, int nqb, int nkb, int kmax,
-                     const int32_t* __restrict__ chunk_cnt, const int32_t* __restrict__ col_at,
-                     int32_t* __restrict__ col_row) {
-  extern __shared__ int32_t place[];
-  const int chunk = blockIdx.x, h = blockIdx.y;
-  const int32_t* cc = chunk_cnt + (static_cast<int64_t>(h) * gridDim.x + chunk) * nkb;
-  const int32_t* at = col_at + static_cast<int64_t>(h) * (nkb + 1);
-  for (int j = threadIdx.x; j < nkb; j += blockDim.x) place[j] = at[j] + cc[j];
-  int32_t* out = col_row + static_cast<int64_t>(h) * nqb * kmax;
-  const int r1 = min(nqb, (chunk + 1) * kMaskRows);
-  for (int i = chunk * kMaskRows; i < r1; ++i) {
-    __syncthreads();  // rows in order
-    const int64_t row = static_cast<int64_t>(h) * nqb + i;
-    const int c = bwd_count(__ldg(cnt + row), kmax);
-    for (int e = threadIdx.x; e < c; e += blockDim.x)
-      out[atomicAdd(&place[bwd_block(__ldg(idx + row * kmax + e), nkb)], 1)] = i;
+  if (threadIdx.x == 0) at[p.nkb] = base;
+  __syncthreads();
+  const int64_t n_words = static_cast<int64_t>(p.n_chunks) * p.nkb;
+  for (int64_t i = threadIdx.x; i < n_words; i += 1024) {
+    const int chunk = static_cast<int>(i / p.nkb), j = static_cast<int>(i - static_cast<int64_t>(chunk) * p.nkb);
+    uint32_t word = words[i];
+    int32_t* out = rows + at[j] + place[i];
+    if (twice[chunk]) {
+      if (word != 0u) bwd_scan_lists(p, h, chunk, j, out);
+    } else {
+      for (; word != 0u; word &= word - 1u) *out++ = chunk * kMaskRows + __ffs(word) - 1;
+    }
   }
 }
 

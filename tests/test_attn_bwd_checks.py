@@ -36,8 +36,9 @@ def test_workspace_size(heads, n_q, n_kv, block, kmax):
     def al(x):
         return (x + 255) // 256 * 256
     nqb, nkb = -(-n_q // block), -(-n_kv // block)
-    want = (256 + 2 * al(heads * nqb * block * 4) + al(heads * -(-nqb // 32) * nkb * 4) + al(heads * (nkb + 1) * 4)
-            + al(heads * nqb * kmax * 4))
+    chunks = -(-nqb // 32)
+    want = (256 + 2 * al(heads * nqb * block * 4) + 2 * al(heads * chunks * nkb * 4) + al(heads * chunks * 4)
+            + al(heads * (nkb + 1) * 4) + al(heads * nqb * kmax * 4))
     assert S.attn_bwd_workspace_size(heads, n_q, n_kv, 128, kmax, block) == want
     with pytest.raises(S.SparstarError):
         S.attn_bwd_workspace_size(heads, n_q, n_kv, 100, kmax, block)

@@ -108,6 +108,17 @@ def test_a_block_listed_twice_counts_twice(S, block):
 
 
 @pytest.mark.parametrize("block", [128, 64])
+def test_blocks_listed_twice_in_some_chunks_of_many_rows(S, block):
+    n_q, n_kv = 70 * block + 3, 9 * block + 1
+    q, k, v, do = inputs(2, n_q, n_kv, 64, 21)
+    idx, cnt = random_lists(2, n_q, n_kv, block, 21)
+    for h, i in ((0, 40), (0, 41), (1, 0), (1, 70)):  # chunks of 32 rows: 1, 1, 0, 2
+        cnt[h, i] = 5
+        idx[h, i, :5] = torch.tensor([4, 9, 4, 0, 9])
+    check(S, do, q, k, v, idx, cnt, block)
+
+
+@pytest.mark.parametrize("block", [128, 64])
 def test_long_lists_of_one_block(S, block):
     """Every query block keeps one and the same KV block: one item walks all of them."""
     q, k, v, do = inputs(2, 6000, 600, 128, 12)
