@@ -124,13 +124,13 @@ __device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
       mbar_init(&b->st_full[i], 1);
       mbar_init(&b->st_empty[i], 1);
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->ds_full[i], 256);
+      mbar_init(&b->ds_full[i], 8);
     }
     mbar_init(&b->held_full, 1);
     mbar_init(&b->held_empty, 1);
-    mbar_init(&b->p_full, 256);
+    mbar_init(&b->p_full, 8);  // one arrival per softmax warp, here and below
     mbar_init(&b->dp_full, 1);
-    mbar_init(&b->dp_read, 256);
+    mbar_init(&b->dp_read, 8);
     mbar_init(&b->acc_full, 1);
   }
   for (int i = 0; i < 2; ++i) {
@@ -138,7 +138,7 @@ __device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
     mbar_init(&bars->item_empty[i], 9);  // the MMA warp and 8 softmax warps
   }
   mbar_init(&bars->smem_free, 1);
-  mbar_init(&bars->tmem_free, 256);
+  mbar_init(&bars->tmem_free, 8);
   mbar_init(&bars->drain, 1);
   bars->abort_flag = 0u;
   fence_barrier_init();
@@ -541,6 +541,12 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsSoftmax));
     // ---------------------------------------------------------- P, dS and the epilogues
+    // One arrival for the warp, after every lane's accesses.
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
     const int half = warp >> 2, wq = warp & 3;
     const int row = wq * 32 + lane;  // row of the held block: KV token, or query token
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
@@ -573,9 +579,9 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (!(ok = wait_all(&bk->st_full[sb], (tk >> 1) & 1u))) break;
           if (!(ok = wait_all(&bk->s_full[0], tk & 1u))) break;
           if (idle) {
-            mbar_arrive(&bk->p_full);
+            arrive(&bk->p_full);
             if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
-            mbar_arrive(&bk->ds_full[0]);
+            arrive(&bk->ds_full[0]);
             continue;
           }
           tc_fence_after();
@@ -594,8 +600,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           }
           bwd_store_half(t_s, pr);
           tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bk->p_full);
+          arrive(&bk->p_full);
           if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
           tc_fence_after();
           bwd_load_half(t_dp, r);
@@ -607,8 +612,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           }
           bwd_store_half(t_dp, pr);
           tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bk->ds_full[0]);
+          arrive(&bk->ds_full[0]);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bk->acc_full, dk_done & 1u))) break;
@@ -620,8 +624,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         const int iq = item - p.n_dkv, h = iq / p.nqb, blk = iq - h * p.nqb;
         if (!in_dq) {
           in_dq = true;
-          tc_fence_before();
-          mbar_arrive(&bars->tmem_free);
+          arrive(&bars->tmem_free);
         }
         const int32_t* list = p.idx + static_cast<int64_t>(iq) * p.kmax;
         const int64_t tok = static_cast<int64_t>(blk) * B + row;
@@ -647,8 +650,8 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (!(ok = wait_all(&bq->s_full[tq & 1u], (tq >> 1) & 1u))) break;
           if (idle) {
             if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
-            mbar_arrive(&bq->dp_read);
-            mbar_arrive(&bq->ds_full[tq & 1u]);
+            arrive(&bq->dp_read);
+            arrive(&bq->ds_full[tq & 1u]);
             continue;
           }
           tc_fence_after();
@@ -667,14 +670,12 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
           tc_fence_after();
           bwd_load_half(t_dp, r);
-          tc_fence_before();
-          mbar_arrive(&bq->dp_read);
+          arrive(&bq->dp_read);
 #pragma unroll
           for (int e = 0; e < 32; ++e) pr[e] = __fmul2_rn(pr[e], __fadd2_rn(bwd_pair(r, e), neg_delta));
           bwd_store_half(t_s, pr);
           tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bq->ds_full[tq & 1u]);
+          arrive(&bq->ds_full[tq & 1u]);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bq->acc_full, dq_done & 1u))) break;
