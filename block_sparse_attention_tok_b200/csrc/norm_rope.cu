@@ -48,7 +48,8 @@ struct NrParams {
   int heads[3];
   float eps;
   unsigned* status;
-  float* dw_part;          // gradient: [CTAs][2][d]
+  float* dw_part;          // gradient: [CTAs of q and k][d]
+  int ctas[3];             // gradient: CTAs of q, k, v
 };
 
 // 8 values of a head vector per lane. Lane l holds 4l.. and d/2 + 4l.. (pairs i, i + d/2), or
@@ -239,62 +240,69 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NrParams p)
   }
 }
 
-// Persistent: each CTA walks items with a fixed stride and keeps the sums of dw of its lanes in
-// registers, so dw costs no traffic until the CTA's one partial row; the rows are added in
-// order by norm_rope_dw_kernel (no atomics: the same inputs give the same bits).
+// Persistent: every CTA serves one kind (shares of the CTAs go by bytes, see nr_bwd_grid) and walks
+// its items with a fixed stride, keeping the sums of dw of its lanes in registers, so dw costs no
+// traffic until the CTA's one partial row; the rows are added in order by norm_rope_dw_kernel (no
+// atomics: the same inputs give the same bits).
+// Three CTAs an SM with four heads an item (80 registers): 18,432 tokens x 32 heads of q, k and v in
+// 207 us, 5.87 TB/s; with two heads an item 260 us, with four CTAs and two heads 224 us, and with the
+// kinds mixed in every CTA (two sums of dw, 128 registers, two CTAs) 256 us.
+constexpr int kNrBwdCtas = 3;
 template <int D, typename T, bool IL, int H>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NrParams p, int64_t n_items) {
+__global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) norm_rope_bwd_kernel(const NrParams p) {
   constexpr int G = D / 8, kGroups = kNrThreads / G;
   __shared__ float part[kGroups][D];
+  griddep_launch_dependents();
   const int l = threadIdx.x % G, g = threadIdx.x / G;
-  const int n_chunks = p.chunks[0] + p.chunks[1] + p.chunks[2];
   const int i0 = Lane8<D, IL>::first(l), i1 = Lane8<D, IL>::second(l);
-  float dwq[8], dwk[8];
+  int kind = 0, first = blockIdx.x;
+  while (kind < 2 && first >= p.ctas[kind]) first -= p.ctas[kind++];
+  const NrView xv = pick(p.x, kind), yv = pick(p.y, kind), dv = pick(p.dx, kind);
+  const int chunks = kind == 0 ? p.chunks[0] : p.chunks[1];  // v has k's heads
+  const int heads = kind == 0 ? p.heads[0] : p.heads[1];
+  const int step = kind == 0 ? p.ctas[0] : kind == 1 ? p.ctas[1] : p.ctas[2];
+  const int n_items = static_cast<int>((p.n_tokens + kGroups - 1) / kGroups) * chunks;
+  const int64_t row0 = kind == 0 ? 0 : p.kv_offset;
+  float dw[8], w[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  for (int64_t t = blockIdx.x; t < n_items; t += gridDim.x) {
-    const int64_t tile = t / n_chunks;
-    const NrItem it = nr_item<H>(p, tile, static_cast<int>(t - tile * n_chunks), kGroups, g);
-    const NrView xv = pick(p.x, it.kind), yv = pick(p.y, it.kind);
-    const int64_t row = it.kind == 0 ? it.n : p.kv_offset + it.n;
-    const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(yv.data) + row * yv.token + it.h0 * yv.head;
+  for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+  load_weight<D, IL>(kind == 0 ? p.w[0] : p.w[1], l, w);
+  for (int t = first; t < n_items; t += step) {
+    const int tile = t / chunks, h0 = (t - tile * chunks) * H;
+    const int64_t n = static_cast<int64_t>(tile) * kGroups + g;
+    const int nh = n < p.n_tokens ? min(H, heads - h0) : 0;
+    const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(yv.data) + (row0 + n) * yv.token + h0 * yv.head;
+    T* dst = static_cast<T*>(dv.data) + n * dv.token + h0 * dv.head;
     Raw8<__nv_bfloat16> rdy[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      if (it.live && h < it.nh)
+      if (h < nh)
         rdy[h].load(dy + h * yv.head, i0, i1);
       else
         rdy[h].zero();
     }
-    const NrView dv = pick(p.dx, it.kind);
-    T* dst = static_cast<T*>(dv.data) + it.n * dv.token + it.h0 * dv.head;
-    if (it.kind == 2) {
+    if (kind == 2) {
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         float d[8];
         rdy[h].get(d);
-        if (it.live && h < it.nh) store8(dst + h * dv.head, i0, i1, d);
+        if (h < nh) store8(dst + h * dv.head, i0, i1, d);
       }
       continue;
     }
-    const T* src = static_cast<const T*>(xv.data) + it.n * xv.token + it.h0 * xv.head;
+    const T* src = static_cast<const T*>(xv.data) + n * xv.token + h0 * xv.head;
     Raw8<T> rx[H];
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      if (it.live && h < it.nh)
+      if (h < nh)
         rx[h].load(src + h * xv.head, i0, i1);
       else
         rx[h].zero();
     }
-    float c[4], s[4], w[8];
-    load_angles<D, IL>(p, it.live ? it.n : 0, l, c, s);
-    load_weight<D, IL>(it.kind == 0 ? p.w[0] : p.w[1], l, w);
+    float c[4], s[4];
+    load_angles<D, IL>(p, nh > 0 ? n : 0, l, c, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[i] = -s[i];
-    // the item's kind is uniform over the CTA: a sum of its own for each keeps it in registers
-    float sum[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[e] = 0.f;
 #pragma unroll
     for (int h = 0; h < H; ++h) {
       float x[8], d[8];
@@ -309,60 +317,62 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_bwd_kernel(const NrParam
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] *= r;
-        sum[e] = fmaf(d[e], x[e], sum[e]);
+        dw[e] = fmaf(d[e], x[e], dw[e]);
         d[e] *= w[e];
         dot = fmaf(d[e], x[e], dot);
       }
       const float m = group_sum<G>(dot) * (1.f / D);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = r * (d[e] - x[e] * m);
-      if (it.live && h < it.nh) store8(dst + h * dv.head, i0, i1, d);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (it.kind == 0)
-        dwq[e] += sum[e];
-      else
-        dwk[e] += sum[e];
+      if (h < nh) store8(dst + h * dv.head, i0, i1, d);
     }
   }
-  for (int kind = 0; kind < 2; ++kind) {
-    __syncthreads();
+  if (kind == 2) return;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      part[g][i0 + e] = kind == 0 ? dwq[e] : dwk[e];
-      part[g][i1 + e] = kind == 0 ? dwq[4 + e] : dwk[4 + e];
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float a = 0.f;
+  for (int e = 0; e < 4; ++e) {
+    part[g][i0 + e] = dw[e];
+    part[g][i1 + e] = dw[4 + e];
+  }
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float a = 0.f;
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) a += part[i][threadIdx.x];
-      p.dw_part[(static_cast<int64_t>(blockIdx.x) * 2 + kind) * D + threadIdx.x] = a;
-    }
+    for (int i = 0; i < kGroups; ++i) a += part[i][threadIdx.x];
+    p.dw_part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = a;  // q's rows, then k's
   }
 }
 
-// dw[d] of kind blockIdx.x = the partial rows in ascending order, split over 1024 / D slices
-// that are added in order at the end.
+// dw[d] of one kind, 32 columns a CTA: 32 warps each add every 32nd partial row of their columns,
+// then the warps' sums are added in order.
 template <int D>
-__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int rows, float* dwq,
-                                                            float* dwk) {
-  constexpr int kSlices = 1024 / D;
-  __shared__ float sum[kSlices][D];
-  float* dw = blockIdx.x == 0 ? dwq : dwk;
+__global__ void __launch_bounds__(1024) norm_rope_dw_kernel(const float* __restrict__ part, int rows_q, int rows_k,
+                                                            float* dwq, float* dwk) {
+  __shared__ float sum[32][33];
+  griddep_wait();
+  const int kind = blockIdx.x & 1, c0 = (blockIdx.x >> 1) * 32;
+  float* dw = kind == 0 ? dwq : dwk;
   if (dw == nullptr) return;
-  const int c = threadIdx.x % D, sl = threadIdx.x / D;
+  const int rows = kind == 0 ? rows_q : rows_k;
+  part += static_cast<int64_t>(kind == 0 ? 0 : rows_q) * D;
+  const int c = threadIdx.x & 31, w = threadIdx.x >> 5;
   float a = 0.f;
-#pragma unroll 4
-  for (int r = sl; r < rows; r += kSlices) a += part[(static_cast<int64_t>(r) * 2 + blockIdx.x) * D + c];
-  sum[sl][c] = a;
+  for (int r0 = w; r0 < rows; r0 += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int r = r0 + 32 * u;
+      v[u] = r < rows ? part[static_cast<int64_t>(r) * D + c0 + c] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a += v[u];
+  }
+  sum[w][c] = a;
   __syncthreads();
-  if (sl == 0) {
+  if (w == 0) {
     a = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSlices; ++i) a += sum[i][c];
-    dw[c] = a;
+    for (int i = 0; i < 32; ++i) a += sum[i][c];
+    dw[c0 + c] = a;
   }
 }
 
@@ -415,6 +425,22 @@ void nr_chunks(NrParams* p, int per) {
 int64_t nr_items(const NrParams& p, int head_dim) {
   const int64_t groups = kNrThreads / (head_dim / 8);
   return (p.n_tokens + groups - 1) / groups * (p.chunks[0] + p.chunks[1] + p.chunks[2]);
+}
+
+// CTAs of the gradient: as many as run at once, shared out to q, k and v by the bytes that each
+// moves (dy, x and dx; v has no x), at most one per item and one per kind that has heads.
+void nr_bwd_grid(NrParams* p, int head_dim, int x_bytes, int per_sm, int sms) {
+  const int64_t groups = kNrThreads / (head_dim / 8), tiles = (p->n_tokens + groups - 1) / groups;
+  const int64_t most = static_cast<int64_t>(per_sm) * sms < kNrMaxParts ? per_sm * sms : kNrMaxParts;
+  const int64_t bytes[3] = {p->heads[0] * (2 + 2 * x_bytes), p->heads[1] * (2 + 2 * x_bytes),
+                            p->heads[2] * (2 + x_bytes)};
+  const int64_t all = bytes[0] + bytes[1] + bytes[2];
+  for (int kind = 0; kind < 3; ++kind) {
+    const int64_t items = tiles * p->chunks[kind];
+    int64_t c = most * bytes[kind] / all;
+    if (c < 1) c = 1;
+    p->ctas[kind] = static_cast<int>(p->heads[kind] == 0 ? 0 : c < items ? c : items);
+  }
 }
 
 // Calls f<D, T, IL>() for the runtime head_dim, type and pairing.
@@ -490,7 +516,7 @@ int sparstar_qk_norm_rope(sparstar_view q, sparstar_view k, sparstar_view v, int
 int sparstar_qk_norm_rope_bwd_workspace_size(int head_dim, size_t* bytes) {
   if (bytes == nullptr) return SPARSTAR_ERR_ARG;
   if (head_dim != 64 && head_dim != 128) return SPARSTAR_ERR_UNSUPPORTED;
-  *bytes = static_cast<size_t>(kNrMaxParts) * 2 * head_dim * sizeof(float);
+  *bytes = static_cast<size_t>(kNrMaxParts) * head_dim * sizeof(float);
   return SPARSTAR_OK;
 }
 
@@ -522,22 +548,27 @@ int sparstar_qk_norm_rope_bwd(sparstar_view dq, sparstar_view dk, sparstar_view 
   p.status = dev->status;
   p.dw_part = static_cast<float*>(workspace);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Four heads an item in bf16; two where fp32 values would not fit the registers, or where few
+  // items leave SMs without one (1,000 tokens x 6 heads fp32: 5.3 us against 6.4 us with four).
   nr_chunks(&p, 4);
-  const bool wide = nr_items(p, head_dim) >= 2 * dev->sms;
-  if (!wide) nr_chunks(&p, 1);
-  const int64_t items = nr_items(p, head_dim);  // 0 tokens: no item, and dw is a sum of nothing
-  const int64_t most = dev->sms * 4 < kNrMaxParts ? dev->sms * 4 : kNrMaxParts;
-  const int grid = static_cast<int>(items < 1 ? 1 : items < most ? items : most);
+  const bool four = x_dtype == SPARSTAR_BF16 && nr_items(p, head_dim) >= kNrBwdCtas * dev->sms;
+  if (!four) nr_chunks(&p, 2);
+  if (nr_items(p, head_dim) > INT32_MAX) return SPARSTAR_ERR_UNSUPPORTED;
+  nr_bwd_grid(&p, head_dim, e, kNrBwdCtas, dev->sms);
+  const int grid = p.ctas[0] + p.ctas[1] + p.ctas[2];  // 0 tokens: none, and dw is a sum of nothing
   nr_dispatch(head_dim, x_dtype, interleaved != 0, [&](auto d, auto t, auto il) {
     using T = decltype(t);
     constexpr int D = decltype(d)::value;
     constexpr bool IL = decltype(il)::value;
-    if (wide)
-      norm_rope_bwd_kernel<D, T, IL, 4><<<grid, kNrThreads, 0, st>>>(p, items);
-    else
-      norm_rope_bwd_kernel<D, T, IL, 1><<<grid, kNrThreads, 0, st>>>(p, items);
+    if (grid > 0 && four) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        norm_rope_bwd_kernel<D, T, IL, 4><<<grid, kNrThreads, 0, st>>>(p);
+    } else if (grid > 0) {
+      norm_rope_bwd_kernel<D, T, IL, 2><<<grid, kNrThreads, 0, st>>>(p);
+    }
     if (dwq != nullptr || dwk != nullptr)
-      norm_rope_dw_kernel<D><<<2, 1024, 0, st>>>(p.dw_part, grid, dwq, dwk);
+      launch_after(norm_rope_dw_kernel<D>, dim3(D / 32 * 2), dim3(1024), 0, st, p.dw_part, p.ctas[0], p.ctas[1], dwq,
+                   dwk);
   });
   return launch_status();
 }

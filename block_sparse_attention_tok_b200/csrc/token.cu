@@ -9,10 +9,10 @@
 // selection with the G heads as the query block.
 //
 // token_kernel is one launch for all of it. A cluster of C CTAs serves one (sequence, key head):
-// they share the scoring (scores go to the first CTA's shared memory), the first CTA ranks and
-// writes the list, each CTA attends to every C-th block of it, and the partial results (max,
-// sum, o of G rows) are merged through distributed shared memory: no workspace, no atomics, the
-// same order of additions every time.
+// each CTA attends to every C-th kept block, and the partial results (max, sum, o of G rows) are
+// merged through distributed shared memory: no workspace, no atomics, the same order of additions
+// every time. Up to 160 candidates (one a thread) every CTA scores and ranks all of them for itself;
+// more are scored by all CTAs into the first one's shared memory, which ranks and writes the list.
 // Bound: memory (4 bytes a scored mean value, 4 bytes a kept K/V value, read once). K and V tiles
 // come by TMA into a ring of shared-memory stages; the products use mma.sync on 16 rows (G real
 // ones): one tile of 64 KB takes the SM about 2,700 cycles to receive and its 256 products a
@@ -37,7 +37,7 @@ namespace {
 constexpr int kTokThreads = 160;      // 4 product warps and a TMA warp
 constexpr int kTokMaxGroup = 16;      // query heads of one key head
 constexpr int kTokMaxBlocks = 16384;  // blocks of one sequence whose scores fit shared memory
-constexpr int kDigitBins = 2048;      // radix select: 11 bits a pass
+constexpr int kDigitBins = 256;       // radix select: 8 bits a pass
 constexpr int kGather = 128;          // a bucket of at most this many keys is ranked directly
 
 template <int D>
@@ -47,7 +47,6 @@ struct TokConfig {
   static constexpr uint32_t kTileBytes = kChunks * kChunkBytes;  // 128 tokens
   static constexpr int kStages = D == 128 ? 3 : 6;               // 96 KB: two CTAs an SM
   static constexpr uint32_t kRingBytes = kStages * kTileBytes;
-  static constexpr uint32_t kFixedBytes = 512;                   // barriers and flags
 };
 
 struct TokParams {
@@ -63,6 +62,15 @@ struct TokParams {
   int hk, group, nb_cap, keep, n_sink, n_recent;
   float scale_log2;
   uint32_t union_bytes;     // shared memory that scores and ring share
+};
+
+// Shared memory behind the ring and the scores.
+struct TokFixed {
+  uint64_t full[6], empty[6];
+  double score[kTokThreads];    // few candidates: scored and ranked by every CTA for itself
+  int32_t chosen[kTokThreads];
+  int32_t warp_tot[kTokThreads / 32];
+  uint32_t abort_flag;
 };
 
 // Order-preserving key of a score: NaN lowest, -0 = +0.
@@ -111,9 +119,8 @@ __device__ void rank_and_write(const double* scores, int n, int take, int base, 
   unsigned long long cut = 0ull;
   int eq = 0;  // how many keys equal to `cut` are taken
   bool done = false, whole = false;  // whole: every key with the cut's looked-at digits is taken
-  for (int shift = 53; !done; shift = shift >= 11 ? shift - 11 : 0) {
-    const int bits = shift >= 9 ? 11 : 9;  // digits at 53, 42, 31, 20, 9, 0
-    const int bins = 1 << bits;
+  constexpr int bins = kDigitBins;
+  for (int shift = 56; !done; shift -= 8) {
     for (int i = tid; i < bins; i += kTokThreads) st->hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kTokThreads) {
@@ -122,7 +129,7 @@ __device__ void rank_and_write(const double* scores, int n, int take, int base, 
     }
     __syncthreads();
     if (w == 0) {  // the digit at which the count from the top reaches `need`
-      const int per = bins / 32;
+      constexpr int per = bins / 32;
       int sum = 0;
       for (int i = 0; i < per; ++i) sum += st->hist[bins - 1 - (lane * per + i)];
       int incl = sum;
@@ -212,6 +219,66 @@ __device__ void rank_and_write(const double* scores, int n, int take, int base, 
   }
 }
 
+// Scores of blocks first, first + step, ... below n (8 lanes a block), each to scores[j]: the sum
+// over the group's queries, times the block's mean, in fp64.
+template <int D>
+__device__ __forceinline__ void score_blocks(const __nv_bfloat16* q, int group, const float* means, int n, int first,
+                                             int step, double* scores) {
+  constexpr int N = D / 32;  // float4 per lane
+  const int l = threadIdx.x & 7;
+  double qs[4 * N];
+#pragma unroll
+  for (int i = 0; i < 4 * N; ++i) qs[i] = 0.0;
+  for (int g = 0; g < group; ++g)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(q + g * D + 4 * (l + 8 * i)));
+      qs[4 * i] += static_cast<double>(__uint_as_float(v.x << 16));
+      qs[4 * i + 1] += static_cast<double>(__uint_as_float(v.x & 0xFFFF0000u));
+      qs[4 * i + 2] += static_cast<double>(__uint_as_float(v.y << 16));
+      qs[4 * i + 3] += static_cast<double>(__uint_as_float(v.y & 0xFFFF0000u));
+    }
+  const float4* mean = reinterpret_cast<const float4*>(means) + l;
+  for (int j0 = first; j0 < n; j0 += step) {
+    const int j = j0 + threadIdx.x / 8;
+    double s = 0.0;
+    if (j < n) {
+      float4 m[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) m[i] = __ldg(mean + static_cast<int64_t>(j) * (D / 4) + 8 * i);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s = fma(qs[4 * i], static_cast<double>(m[i].x), s);
+        s = fma(qs[4 * i + 1], static_cast<double>(m[i].y), s);
+        s = fma(qs[4 * i + 2], static_cast<double>(m[i].z), s);
+        s = fma(qs[4 * i + 3], static_cast<double>(m[i].w), s);
+      }
+    }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+    if (l == 0 && j < n) scores[j] = s;
+  }
+}
+
+// At most one candidate a thread: its rank is the number of better ones. The chosen positions go,
+// ascending, to chosen. One CTA, all threads, scores written before (and synchronised).
+__device__ __forceinline__ void rank_few(const double* scores, int n, int take, int32_t* chosen, int32_t* warp_tot) {
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const unsigned long long key = tid < n ? score_key(scores[tid]) : 0ull;
+  int above = 0;
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long k = score_key(scores[i]);
+    above += k > key || (k == key && i < tid);
+  }
+  const bool take_it = tid < n && above < take;
+  const unsigned b = __ballot_sync(0xFFFFFFFFu, take_it);
+  if (lane == 0) warp_tot[w] = __popc(b);
+  __syncthreads();
+  int pos = __popc(b & ((1u << lane) - 1u));
+  for (int x = 0; x < w; ++x) pos += warp_tot[x];
+  if (take_it) chosen[pos] = tid;
+}
+
 // SEL: choose the blocks (idx, cnt are written). ATT: attend to them (with SEL to the chosen
 // ones, else to the given idx, cnt). grid (C, Hk, B), clusters of C along x.
 template <int D, bool SEL, bool ATT>
@@ -226,9 +293,9 @@ __global__ void __launch_bounds__(kTokThreads)
   const int hk = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = static_cast<int64_t>(b) * p.hk + hk;  // (sequence, key head)
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.union_bytes);
-  uint64_t* empty = full + C::kStages;
-  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(empty + C::kStages);
+  TokFixed* fix = reinterpret_cast<TokFixed*>(smem + p.union_bytes);
+  uint64_t *full = fix->full, *empty = fix->empty;
+  volatile uint32_t* abort_flag = &fix->abort_flag;
 
   int64_t len = __ldg(p.kv_len + b);
   if (len < 0 || len > p.capacity) {
@@ -244,84 +311,57 @@ __global__ void __launch_bounds__(kTokThreads)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
     }
-    *const_cast<uint32_t*>(abort_flag) = 0u;
+    fix->abort_flag = 0u;
     fence_barrier_init();
   }
 
-  if (SEL) {
-    const int n_cand = nb - p.n_sink - p.n_recent;
-    if (nb <= p.keep) {
-      if (rank == 0) {
-        for (int e = tid; e < p.keep; e += kTokThreads) list[e] = e < nb ? e : -1;
-        if (tid == 0) p.cnt[row] = nb;
-      }
+  // Where the e-th kept block stands: every block (all), forced and chosen ones (few candidates,
+  // ranked by every CTA), or the list that the first CTA wrote.
+  const int n_cand = nb - p.n_sink - p.n_recent, take = p.keep - p.n_sink - p.n_recent;
+  const bool all = SEL && nb <= p.keep, few = SEL && !all && n_cand <= kTokThreads;
+  bool synced = false;
+  if (SEL && !all && take > 0) {  // 0 < take < n_cand
+    const float* means = p.means + (row * p.nb_cap + p.n_sink) * D;
+    if (few) {
+      score_blocks<D>(q, p.group, means, n_cand, 0, kTokThreads / 8, fix->score);
+      __syncthreads();
+      rank_few(fix->score, n_cand, take, fix->chosen, fix->warp_tot);
+      __syncthreads();
     } else {
-      const int take = p.keep - p.n_sink - p.n_recent;
-      if (take > 0) {  // 0 < take < n_cand
-        if (size > 1) cluster.sync();  // the first CTA runs before anyone writes to it
-        double* scores = cluster.map_shared_rank(reinterpret_cast<double*>(smem), 0);
-        // 8 lanes a block, each holding D / 8 values of the query sum
-        constexpr int N = D / 32;  // float4 per lane
-        const int l = lane & 7;
-        double qs[4 * N];
-#pragma unroll
-        for (int i = 0; i < 4 * N; ++i) qs[i] = 0.0;
-        for (int g = 0; g < p.group; ++g)
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(q + g * D + 4 * (l + 8 * i)));
-            qs[4 * i] += static_cast<double>(__uint_as_float(v.x << 16));
-            qs[4 * i + 1] += static_cast<double>(__uint_as_float(v.x & 0xFFFF0000u));
-            qs[4 * i + 2] += static_cast<double>(__uint_as_float(v.y << 16));
-            qs[4 * i + 3] += static_cast<double>(__uint_as_float(v.y & 0xFFFF0000u));
-          }
-        const float4* mean = reinterpret_cast<const float4*>(p.means + (row * p.nb_cap + p.n_sink) * D) + l;
-        constexpr int kPer = kTokThreads / 8;  // blocks a CTA scores at a time
-        for (int j0 = rank * kPer; j0 < n_cand; j0 += size * kPer) {
-          const int j = j0 + tid / 8;
-          double s = 0.0;
-          if (j < n_cand) {
-            float4 m[N];
-#pragma unroll
-            for (int i = 0; i < N; ++i) m[i] = __ldg(mean + static_cast<int64_t>(j) * (D / 4) + 8 * i);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-              s = fma(qs[4 * i], static_cast<double>(m[i].x), s);
-              s = fma(qs[4 * i + 1], static_cast<double>(m[i].y), s);
-              s = fma(qs[4 * i + 2], static_cast<double>(m[i].z), s);
-              s = fma(qs[4 * i + 3], static_cast<double>(m[i].w), s);
-            }
-          }
-#pragma unroll
-          for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-          if (l == 0 && j < n_cand) scores[j] = s;
-        }
-        if (size > 1)
-          cluster.sync();
-        else
-          __syncthreads();
-        if (rank == 0) {
-          const double* mine = reinterpret_cast<const double*>(smem);
-          RankState* st = reinterpret_cast<RankState*>(smem + ((static_cast<size_t>(n_cand) * 8 + 15) & ~15ull));
-          rank_and_write(mine, n_cand, take, p.n_sink, list + p.n_sink, st);
-        }
-      }
+      if (size > 1) cluster.sync();  // the first CTA runs before anyone writes to it
+      constexpr int kPer = kTokThreads / 8;  // blocks a CTA scores at a time
+      score_blocks<D>(q, p.group, means, n_cand, rank * kPer, size * kPer,
+                      cluster.map_shared_rank(reinterpret_cast<double*>(smem), 0));
+      if (size > 1)
+        cluster.sync();
+      else
+        __syncthreads();
       if (rank == 0) {
-        for (int e = tid; e < p.n_sink; e += kTokThreads) list[e] = e;
-        for (int e = tid; e < p.n_recent; e += kTokThreads) list[p.keep - p.n_recent + e] = nb - p.n_recent + e;
-        if (tid == 0) p.cnt[row] = p.keep;
+        RankState* st = reinterpret_cast<RankState*>(smem + ((static_cast<size_t>(n_cand) * 8 + 15) & ~15ull));
+        rank_and_write(reinterpret_cast<const double*>(smem), n_cand, take, p.n_sink, list + p.n_sink, st);
+      }
+      if (size > 1) {
+        cluster.sync();  // the list is written
+        synced = true;
       }
     }
   }
-  if (!ATT) {
-    if (size > 1) cluster.sync();  // remote stores into the first CTA are over
-    return;
+  auto kept_at = [&](int e) {  // SEL, unless the list has it
+    return all ? e
+               : e < p.n_sink ? e
+                              : e >= p.keep - p.n_recent ? nb - p.keep + e : p.n_sink + fix->chosen[e - p.n_sink];
+  };
+  if (SEL && rank == 0) {
+    if (all) {
+      for (int e = tid; e < p.keep; e += kTokThreads) list[e] = e < nb ? e : -1;
+    } else {
+      for (int e = tid; e < p.keep; e += kTokThreads)
+        if (few || e < p.n_sink || e >= p.keep - p.n_recent) list[e] = kept_at(e);
+    }
+    if (tid == 0) p.cnt[row] = all ? nb : p.keep;
   }
-  // list, cnt and barriers are ready for every CTA of the cluster
-  if (size > 1)
-    cluster.sync();
-  else
-    __syncthreads();
+  if (!ATT) return;
+  if (!synced) __syncthreads();  // barriers, the list of a lone CTA
 
   int n_ent = SEL ? (nb <= p.keep ? nb : p.keep) : __ldg(p.cnt + row);
   if (!SEL && (n_ent < 0 || n_ent > p.keep)) {
@@ -331,7 +371,10 @@ __global__ void __launch_bounds__(kTokThreads)
   const int n_mine = n_ent > rank ? (n_ent - rank + size - 1) / size : 0;
   // Block of this CTA's i-th entry, or -1 (recorded) where it names no block that holds tokens.
   auto block_at = [&](int i, bool report) {
-    const int j = *const_cast<volatile int32_t*>(list + rank + i * size);
+    const int e = rank + i * size;
+    const int j = SEL && (all || few || e < p.n_sink || e >= p.keep - p.n_recent)
+                      ? kept_at(e)
+                      : *const_cast<volatile int32_t*>(list + e);
     if (j < 0 || j >= nb) {
       if (report) atomicOr(p.status, kStatusBounds);
       return -1;
@@ -610,7 +653,7 @@ uint32_t tok_union_bytes(int d, int64_t nb, bool sel, bool att) {
 
 template <int D>
 int tok_set_attrs() {
-  const uint32_t most = tok_union_bytes(D, kTokMaxBlocks, true, true) + 1024 + TokConfig<D>::kFixedBytes;
+  const uint32_t most = tok_union_bytes(D, kTokMaxBlocks, true, true) + 1024 + sizeof(TokFixed);
   for (auto kernel : {token_kernel<D, true, true>, token_kernel<D, true, false>, token_kernel<D, false, true>})
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
       return SPARSTAR_ERR_CUDA;
@@ -689,7 +732,7 @@ int token_run(bool sel, bool att, const void* q, const void* k, const void* v, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, static_cast<unsigned>(heads_k), static_cast<unsigned>(n_seq));
   cfg.blockDim = dim3(kTokThreads);
-  cfg.dynamicSmemBytes = p.union_bytes + 1024 + TokConfig<128>::kFixedBytes;
+  cfg.dynamicSmemBytes = p.union_bytes + 1024 + sizeof(TokFixed);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -11,7 +11,7 @@ at most 12 roundings and the two errors: below 30 u of its sum of absolute value
 and the product by r add 3 u and r's own 10 u: below 64 u = 2^-18 of
 r (|g|_max + |xh| mean(|g|_max |xh|)), |g|_max = |w| (|a| + |b|). A bf16 output adds 2^-8 of the value.
 dw: each term has below 16 u of (|a| + |b|) |xh|; the sum's longest chain is (terms of a lane) +
-(32 groups at most) + (rows of a slice, at most 1024 / 8) + 16 slices.
+(32 groups at most) + (32 rows of a slice at most) + 32 slices.
 """
 import torch
 
@@ -72,10 +72,10 @@ def backward(x, dy, w, cos, sin, eps, interleaved, out_dtype):
 
 
 def dw_tol(n, heads, d, sums):
-    """Bound of dw's error from its terms' sums of absolute values (see above): a lane of the
-    smallest grid (one CTA) would add every item's terms, so the chain is bounded by what 592 CTAs
-    of 4 heads leave to a lane."""
+    """Bound of dw's error from its terms' sums of absolute values (see above). A lane adds up to
+    four terms of every item of its CTA; with at least 50 of the 444 CTAs (3 an SM) for a kind that
+    moves a ninth of the bytes or more, as the cases here do, that is 4 (items / 50 + 1) at most."""
     groups = 256 // (d // 8)
-    items = -(-n // groups) * (-(-heads // 4) + 2)
-    chain = 4 * (-(-items // 592) + 1) + 32 + 128 + 16
+    items = -(-n // groups) * -(-heads // 2)
+    chain = 4 * (-(-items // 50) + 1) + 32 + 32 + 32
     return (16 + chain) * U * sums + 1e-30
