@@ -1,8 +1,7 @@
 // One query token per sequence over a K/V cache: block means, selection, attention.
 //
 // Per (sequence, key head), with G = heads_q / heads_k query heads that share the key head:
-//   score_j = (sum_g q_g) . mean_j      of every block j between the forced ones (fp64: the rank
-//                                       of two near scores must not hang on a summation order),
+//   score_j = (sum_g q_g) . mean_j      of every block j between the forced ones,
 //   kept    = the first n_sink and last n_recent blocks and the best others up to `keep`,
 //   o_g     = sum over the kept tokens u of softmax_u(s q_g . k_u) v_u,  lse_g.
 // The mean of the G queries ranks as their sum does, so this is the block score of the scale's
@@ -13,6 +12,7 @@
 // merged through distributed shared memory: no workspace, no atomics, the same order of additions
 // every time. Up to 160 candidates (one a thread) every CTA scores and ranks all of them for itself;
 // more are scored by all CTAs into the first one's shared memory, which ranks and writes the list.
+// The forced blocks are attended to first: their tiles are on the way while the others are ranked.
 // Bound: memory (4 bytes a scored mean value, 4 bytes a kept K/V value, read once). K and V tiles
 // come by TMA into a ring of shared-memory stages; the products use mma.sync on 16 rows (G real
 // ones): one tile of 64 KB takes the SM about 2,700 cycles to receive and its 256 products a
@@ -38,7 +38,7 @@ constexpr int kTokThreads = 160;      // 4 product warps and a TMA warp
 constexpr int kTokMaxGroup = 16;      // query heads of one key head
 constexpr int kTokMaxBlocks = 16384;  // blocks of one sequence whose scores fit shared memory
 constexpr int kDigitBins = 256;       // radix select: 8 bits a pass
-constexpr int kGather = 128;          // a bucket of at most this many keys is ranked directly
+constexpr int kFew = kTokThreads;     // candidates that are ranked by counting, one a thread
 
 template <int D>
 struct TokConfig {
@@ -61,17 +61,30 @@ struct TokParams {
   int64_t capacity;
   int hk, group, nb_cap, keep, n_sink, n_recent;
   float scale_log2;
-  uint32_t union_bytes;     // shared memory that scores and ring share
+  uint32_t score_at;        // where scores lie: behind the ring, or (0) in its place where they are many
+  uint32_t fixed_at;        // TokFixed, behind both
+};
+
+// What a CTA's threads tell one another while ranking.
+struct RankShared {
+  int32_t tot[2][kTokThreads / 32];
+  float most[kTokThreads / 32];
+  float cut;
 };
 
 // Shared memory behind the ring and the scores.
 struct TokFixed {
   uint64_t full[6], empty[6];
-  double score[kTokThreads];    // few candidates: scored and ranked by every CTA for itself
-  int32_t chosen[kTokThreads];
-  int32_t warp_tot[kTokThreads / 32];
+  // few candidates: scored and ranked by every CTA for itself
+  float2 fast[kFew];
+  uint32_t key[kFew];
+  double exact[kFew];
+  int32_t chosen[kFew], near[kFew];
+  RankShared rank;
   uint32_t abort_flag;
 };
+
+static_assert(sizeof(TokFixed) <= 6144, "two CTAs an SM");
 
 // Order-preserving key of a score: NaN lowest, -0 = +0.
 __device__ __forceinline__ unsigned long long score_key(double s) {
@@ -99,39 +112,35 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Shared state of the ranking, behind the scores.
+// Shared state of the radix select, behind the scores.
 struct RankState {
   int32_t hist[kDigitBins];
-  unsigned long long keys[kGather];
-  int32_t warp_tot[2][kTokThreads / 32];
-  unsigned long long cut;
-  int32_t need, bucket, count, eq;
+  int32_t need, bucket;
 };
 
-// Ranks scores[0, n) and writes the `take` best as base + position, ascending, to out. One CTA,
-// all threads. Equal scores go to the lower position.
-__device__ void rank_and_write(const double* scores, int n, int take, int base, int32_t* out, RankState* st) {
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  // Radix select of the take-th largest key, from the top digit down, until the bucket that
-  // holds it is taken whole or small enough to be ranked by counting.
+struct KthKey {
+  unsigned long long key;  // the take-th largest key
+  int equal;               // how many of the keys equal to it are among the take largest
+};
+
+// Radix select over key(0..n), from the digit at `shift` (8 bits) down. One CTA, all threads.
+template <typename F>
+__device__ KthKey kth_key(int n, int take, int shift, RankState* st, F&& key) {
+  const int tid = threadIdx.x, lane = tid & 31;
   unsigned long long prefix = 0ull, mask = 0ull;
   int need = take;
-  unsigned long long cut = 0ull;
-  int eq = 0;  // how many keys equal to `cut` are taken
-  bool done = false, whole = false;  // whole: every key with the cut's looked-at digits is taken
-  constexpr int bins = kDigitBins;
-  for (int shift = 56; !done; shift -= 8) {
-    for (int i = tid; i < bins; i += kTokThreads) st->hist[i] = 0;
+  for (; shift >= 0; shift -= 8) {
+    for (int i = tid; i < kDigitBins; i += kTokThreads) st->hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < n; i += kTokThreads) {
-      const unsigned long long key = score_key(scores[i]);
-      if ((key & mask) == prefix) atomicAdd(&st->hist[(key >> shift) & (bins - 1)], 1);
+      const unsigned long long k = key(i);
+      if ((k & mask) == prefix) atomicAdd(&st->hist[(k >> shift) & (kDigitBins - 1)], 1);
     }
     __syncthreads();
-    if (w == 0) {  // the digit at which the count from the top reaches `need`
-      constexpr int per = bins / 32;
+    if (tid < 32) {  // the digit at which the count from the top reaches `need`
+      constexpr int per = kDigitBins / 32;
       int sum = 0;
-      for (int i = 0; i < per; ++i) sum += st->hist[bins - 1 - (lane * per + i)];
+      for (int i = 0; i < per; ++i) sum += st->hist[kDigitBins - 1 - (lane * per + i)];
       int incl = sum;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -141,10 +150,9 @@ __device__ void rank_and_write(const double* scores, int n, int take, int base, 
       int above = incl - sum;
       if (above < need && need <= incl) {
         for (int i = 0;; ++i) {
-          const int b = bins - 1 - (lane * per + i), c = st->hist[b];
+          const int b = kDigitBins - 1 - (lane * per + i), c = st->hist[b];
           if (above + c >= need) {
             st->bucket = b;
-            st->count = c;
             st->need = need - above;
             break;
           }
@@ -154,129 +162,275 @@ __device__ void rank_and_write(const double* scores, int n, int take, int base, 
     }
     __syncthreads();
     prefix |= static_cast<unsigned long long>(st->bucket) << shift;
-    mask |= static_cast<unsigned long long>(bins - 1) << shift;
+    mask |= static_cast<unsigned long long>(kDigitBins - 1) << shift;
     need = st->need;
-    const int count = st->count;
-    if (count == need) {
-      cut = prefix;
-      eq = count;
-      done = whole = true;
-    } else if (shift == 0) {  // equal keys, of which `need` are taken
-      cut = prefix;
-      eq = need;
-      done = true;
-    } else if (count <= kGather) {
-      __syncthreads();
-      if (tid == 0) st->count = 0;
-      __syncthreads();
-      for (int i = tid; i < n; i += kTokThreads) {
-        const unsigned long long key = score_key(scores[i]);
-        if ((key & mask) == prefix) st->keys[atomicAdd(&st->count, 1)] = key;
-      }
-      __syncthreads();
-      if (tid < count) {
-        const unsigned long long key = st->keys[tid];
-        int above = 0, same = 0;
-        for (int i = 0; i < count; ++i) {
-          above += st->keys[i] > key;
-          same += st->keys[i] == key;
-        }
-        if (above < need && need <= above + same) {  // equal keys write equal values
-          st->cut = key;
-          st->eq = need - above;
-        }
-      }
-      __syncthreads();
-      cut = st->cut;
-      eq = st->eq;
-      done = true;
-    }
     __syncthreads();
   }
-  int placed = 0, eq_seen = 0;
-  for (int i0 = 0; i0 < n; i0 += kTokThreads) {
-    const int i = i0 + tid;
-    const unsigned long long key = i < n ? score_key(scores[i]) : 0ull;
-    const bool same = i < n && (whole ? (key & mask) == prefix : key == cut);
-    const bool more = i < n && !same && key > cut;
-    const unsigned bs = __ballot_sync(0xFFFFFFFFu, same);
-    if (lane == 0) st->warp_tot[0][w] = __popc(bs);
-    __syncthreads();
-    int before = eq_seen + __popc(bs & ((1u << lane) - 1u));
-    for (int x = 0; x < w; ++x) before += st->warp_tot[0][x];
-    const bool take_it = more || (same && before < eq);
-    const unsigned bt = __ballot_sync(0xFFFFFFFFu, take_it);
-    if (lane == 0) st->warp_tot[1][w] = __popc(bt);
-    __syncthreads();
-    int pos = placed + __popc(bt & ((1u << lane) - 1u));
-    for (int x = 0; x < w; ++x) pos += st->warp_tot[1][x];
-    if (take_it) out[pos] = base + i;
-    for (int x = 0; x < kTokThreads / 32; ++x) {
-      eq_seen += st->warp_tot[0][x];
-      placed += st->warp_tot[1][x];
-    }
-    __syncthreads();
-  }
+  return KthKey{prefix, need};
 }
 
-// Scores of blocks first, first + step, ... below n (8 lanes a block), each to scores[j]: the sum
-// over the group's queries, times the block's mean, in fp64.
+// Scores in two steps. The fp32 score s_j is off the exact S_j by at most E = 2^-18 max_j B_j, B_j the
+// sum of the absolute products: 15 roundings of the query sum, the product, 19 of the sum, below
+// 36 u = 2^-18.8 of B_j. With t the take-th largest s_j, the take-th largest S_j lies in [t - E, t + E],
+// so s_j > t + 2E is in, s_j < t - 2E is out, and only what lies between (usually t's own block) is
+// scored again, in fp64, where neighbours need it. Scores that are not finite make E so, and every
+// block lies between. (48 sequences x 8 key heads, 297 candidates each: the selection alone takes 22 us,
+// with every score in fp64 36 us, most of it conversions of the means.)
+constexpr float kScoreMargin = 2.25f / 262144.f;  // 2E / max B, with room for the comparison's rounding
+
+__device__ __forceinline__ uint32_t score_key32(float s) {
+  if (isnan(s)) return 0u;
+  const uint32_t b = __float_as_uint(s + 0.f);
+  return (b >> 31) ? ~b : b | 0x80000000u;
+}
+
+// (s, B) of blocks first, first + 1, ... (8 lanes a block, 20 at a time), the next ones step further on,
+// below n.
 template <int D>
-__device__ __forceinline__ void score_blocks(const __nv_bfloat16* q, int group, const float* means, int n, int first,
-                                             int step, double* scores) {
+__device__ __forceinline__ void score_fast(const __nv_bfloat16* q, int group, const float* means, int n, int first,
+                                           int step, float2* scores) {
   constexpr int N = D / 32;  // float4 per lane
-  const int l = threadIdx.x & 7;
-  double qs[4 * N];
+  const int l = threadIdx.x & 7, mine = threadIdx.x / 8;
+  float qs[4 * N], qa[4 * N];
 #pragma unroll
-  for (int i = 0; i < 4 * N; ++i) qs[i] = 0.0;
+  for (int i = 0; i < 4 * N; ++i) qs[i] = qa[i] = 0.f;
   for (int g = 0; g < group; ++g)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const uint2 v = __ldg(reinterpret_cast<const uint2*>(q + g * D + 4 * (l + 8 * i)));
-      qs[4 * i] += static_cast<double>(__uint_as_float(v.x << 16));
-      qs[4 * i + 1] += static_cast<double>(__uint_as_float(v.x & 0xFFFF0000u));
-      qs[4 * i + 2] += static_cast<double>(__uint_as_float(v.y << 16));
-      qs[4 * i + 3] += static_cast<double>(__uint_as_float(v.y & 0xFFFF0000u));
-    }
-  const float4* mean = reinterpret_cast<const float4*>(means) + l;
-  for (int j0 = first; j0 < n; j0 += step) {
-    const int j = j0 + threadIdx.x / 8;
-    double s = 0.0;
-    if (j < n) {
-      float4 m[N];
+      const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                          __uint_as_float(v.y & 0xFFFF0000u)};
 #pragma unroll
-      for (int i = 0; i < N; ++i) m[i] = __ldg(mean + static_cast<int64_t>(j) * (D / 4) + 8 * i);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        s = fma(qs[4 * i], static_cast<double>(m[i].x), s);
-        s = fma(qs[4 * i + 1], static_cast<double>(m[i].y), s);
-        s = fma(qs[4 * i + 2], static_cast<double>(m[i].z), s);
-        s = fma(qs[4 * i + 3], static_cast<double>(m[i].w), s);
+      for (int e = 0; e < 4; ++e) {
+        qs[4 * i + e] += x[e];
+        qa[4 * i + e] += fabsf(x[e]);
       }
     }
+  const float4* mean = reinterpret_cast<const float4*>(means) + l;
+  // four blocks' means in flight per lane
+  for (int j0 = first; j0 < n; j0 += 4 * step) {
+    float4 m[4][N];
 #pragma unroll
-    for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    if (l == 0 && j < n) scores[j] = s;
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * step + mine;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        m[u][i] = j < n ? __ldg(mean + static_cast<int64_t>(j) * (D / 4) + 8 * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int j = j0 + u * step + mine;
+      if (j0 + u * step >= n) break;
+      float s = 0.f, a = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float x[4] = {m[u][i].x, m[u][i].y, m[u][i].z, m[u][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s = fmaf(qs[4 * i + e], x[e], s);
+          a = fmaf(qa[4 * i + e], fabsf(x[e]), a);
+        }
+      }
+#pragma unroll
+      for (int off = 4; off > 0; off >>= 1) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+        a += __shfl_xor_sync(0xFFFFFFFFu, a, off);
+      }
+      if (l == 0 && j < n) scores[j] = make_float2(s, a);
+    }
   }
 }
 
-// At most one candidate a thread: its rank is the number of better ones. The chosen positions go,
-// ascending, to chosen. One CTA, all threads, scores written before (and synchronised).
-__device__ __forceinline__ void rank_few(const double* scores, int n, int take, int32_t* chosen, int32_t* warp_tot) {
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const unsigned long long key = tid < n ? score_key(scores[tid]) : 0ull;
-  int above = 0;
-  for (int i = 0; i < n; ++i) {
-    const unsigned long long k = score_key(scores[i]);
-    above += k > key || (k == key && i < tid);
+// The fp64 score of one block, by 8 lanes (all of a warp take part).
+template <int D>
+__device__ double score_exact(const __nv_bfloat16* q, int group, const float* mean) {
+  const int l = threadIdx.x & 7;
+  double s = 0.0;
+  for (int c = 4 * l; c < D; c += 32) {
+    const float4 m = __ldg(reinterpret_cast<const float4*>(mean + c));
+    const float x[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      double qs = 0.0;
+      for (int g = 0; g < group; ++g) qs += static_cast<double>(__bfloat162float(q[g * D + c + e]));
+      s = fma(qs, static_cast<double>(x[e]), s);
+    }
   }
-  const bool take_it = tid < n && above < take;
-  const unsigned b = __ballot_sync(0xFFFFFFFFu, take_it);
-  if (lane == 0) warp_tot[w] = __popc(b);
+#pragma unroll
+  for (int off = 4; off > 0; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  return s;
+}
+
+// Exact scores of the n blocks near[0..n) (null: 0..n), to out.
+template <int D>
+__device__ void score_all_exact(const __nv_bfloat16* q, int group, const float* means, const int32_t* near, int n,
+                                double* out) {
+  for (int i0 = 0; i0 < n; i0 += kTokThreads / 8) {
+    const int i = i0 + threadIdx.x / 8, at = i < n ? i : n - 1;
+    const double s = score_exact<D>(q, group, means + static_cast<int64_t>(near != nullptr ? near[at] : at) * D);
+    if ((threadIdx.x & 7) == 0 && i < n) out[i] = s;
+  }
+}
+
+// Positions among the `n` exact scores, one a thread: is this thread's one of the `take` best?
+__device__ __forceinline__ bool best_exact(const double* exact, int n, int take) {
+  const unsigned long long key = static_cast<int>(threadIdx.x) < n ? score_key(exact[threadIdx.x]) : 0ull;
+  int above = 0;
+  for (int i = 0; i < n; ++i) above += score_key(exact[i]) + (i < static_cast<int>(threadIdx.x) ? 1u : 0u) > key;
+  return static_cast<int>(threadIdx.x) < n && above < take;
+}
+
+// Two counts over the CTA: lower threads' flags a and b go to before_a, before_b; totals to *all_a, *all_b.
+__device__ __forceinline__ void count2(RankShared* st, bool a, bool b, int* before_a, int* before_b, int* all_a,
+                                       int* all_b) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const unsigned ba = __ballot_sync(0xFFFFFFFFu, a), bb = __ballot_sync(0xFFFFFFFFu, b), low = (1u << lane) - 1u;
+  if (lane == 0) {
+    st->tot[0][w] = __popc(ba);
+    st->tot[1][w] = __popc(bb);
+  }
   __syncthreads();
-  int pos = __popc(b & ((1u << lane) - 1u));
-  for (int x = 0; x < w; ++x) pos += warp_tot[x];
-  if (take_it) chosen[pos] = tid;
+  *before_a = __popc(ba & low);
+  *before_b = __popc(bb & low);
+  *all_a = *all_b = 0;
+#pragma unroll
+  for (int x = 0; x < kTokThreads / 32; ++x) {
+    if (x < w) {
+      *before_a += st->tot[0][x];
+      *before_b += st->tot[1][x];
+    }
+    *all_a += st->tot[0][x];
+    *all_b += st->tot[1][x];
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ float max_over_cta(RankShared* st, float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float o = __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    v = (isnan(v) || v > o) ? v : o;  // NaN stays
+  }
+  if ((threadIdx.x & 31) == 0) st->most[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = st->most[0];
+#pragma unroll
+  for (int x = 1; x < kTokThreads / 32; ++x) v = (isnan(v) || v > st->most[x]) ? v : st->most[x];
+  __syncthreads();
+  return v;
+}
+
+// Class of a score against the cut: 2 in, 1 between, 0 out.
+__device__ __forceinline__ int score_class(float s, float cut, float margin) {
+  if (!isfinite(margin)) return 1;
+  return s - cut > margin ? 2 : s - cut >= -margin ? 1 : 0;
+}
+
+// Ranks up to kFew candidates, one a thread (of equal ones the lower is better: its key counts as one
+// more). The chosen positions go, ascending, to fix->chosen. One CTA, all threads.
+template <int D>
+__device__ __forceinline__ void rank_few(TokFixed* fix, const __nv_bfloat16* q, int group, const float* means, int n,
+                                         int take) {
+  const int tid = threadIdx.x;
+  const bool in = tid < n;
+  const float2 v = in ? fix->fast[tid] : make_float2(0.f, 0.f);
+  const uint32_t key = in ? score_key32(v.x) : 0u;
+  fix->key[tid] = key;
+  const float margin = max_over_cta(&fix->rank, v.y) * kScoreMargin;
+  int above = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) above += fix->key[i] + (i < tid ? 1u : 0u) > key;
+  if (in && above == take - 1) fix->rank.cut = v.x;
+  __syncthreads();
+  const int cls = in ? score_class(v.x, fix->rank.cut, margin) : 0;
+  int before_sure, before_near, sure, near;
+  count2(&fix->rank, cls == 2, cls == 1, &before_sure, &before_near, &sure, &near);
+  bool mine = cls != 0;
+  if (sure + near != take) {
+    if (cls == 1) fix->near[before_near] = tid;
+    __syncthreads();
+    score_all_exact<D>(q, group, means, fix->near, near, fix->exact);
+    __syncthreads();
+    if (best_exact(fix->exact, near, take - sure))
+      fix->chosen[tid] = 1;
+    else
+      fix->chosen[tid] = 0;
+    __syncthreads();
+    mine = cls == 2 || (cls == 1 && fix->chosen[before_near] != 0);
+    __syncthreads();
+  }
+  int before, none, all;
+  count2(&fix->rank, mine, false, &before, &none, &all, &none);
+  if (mine) fix->chosen[before] = tid;
+}
+
+// The same for many candidates, whose fp32 scores one CTA holds; writes base + position to out. With more
+// than kFew blocks between, all are scored exactly (over the fp32 scores) and ranked by their fp64 keys.
+template <int D>
+__device__ void rank_many(float2* scores, TokFixed* fix, RankState* st, const __nv_bfloat16* q, int group,
+                          const float* means, int n, int take, int base, int32_t* out) {
+  const int tid = threadIdx.x;
+  float most = 0.f;
+  for (int i = tid; i < n; i += kTokThreads) most = (isnan(most) || most > scores[i].y) ? most : scores[i].y;
+  const float margin = max_over_cta(&fix->rank, most) * kScoreMargin;
+  bool all_exact = !isfinite(margin);
+  if (!all_exact) {
+    const uint32_t cut_key = static_cast<uint32_t>(
+        kth_key(n, take, 24, st, [&](int i) { return static_cast<unsigned long long>(score_key32(scores[i].x)); }).key);
+    const float cut = __uint_as_float((cut_key >> 31) ? cut_key & 0x7FFFFFFFu : ~cut_key);
+    int sure = 0, near = 0;
+    for (int i0 = 0; i0 < n; i0 += kTokThreads) {
+      const int i = i0 + tid;
+      const int cls = i < n ? score_class(scores[i].x, cut, margin) : 0;
+      int before_sure, before_near, more_sure, more_near;
+      count2(&fix->rank, cls == 2, cls == 1, &before_sure, &before_near, &more_sure, &more_near);
+      if (cls == 1 && near + before_near < kFew) fix->near[near + before_near] = i;
+      sure += more_sure;
+      near += more_near;
+    }
+    all_exact = near > kFew;
+    if (!all_exact) {
+      __syncthreads();
+      fix->chosen[tid] = 1;
+      if (sure + near != take) {
+        score_all_exact<D>(q, group, means, fix->near, near, fix->exact);
+        __syncthreads();
+        fix->chosen[tid] = best_exact(fix->exact, near, take - sure);
+      }
+      __syncthreads();
+      int placed = 0, seen = 0;
+      for (int i0 = 0; i0 < n; i0 += kTokThreads) {
+        const int i = i0 + tid;
+        const int cls = i < n ? score_class(scores[i].x, cut, margin) : 0;
+        int before, before_near, none, more, more_near;
+        count2(&fix->rank, false, cls == 1, &none, &before_near, &none, &more_near);
+        const bool mine = cls == 2 || (cls == 1 && fix->chosen[seen + before_near] != 0);
+        count2(&fix->rank, mine, false, &before, &none, &more, &none);
+        if (mine) out[placed + before] = base + i;
+        placed += more;
+        seen += more_near;
+      }
+      return;
+    }
+  }
+  double* exact = reinterpret_cast<double*>(scores);
+  __syncthreads();
+  score_all_exact<D>(q, group, means, nullptr, n, exact);
+  __syncthreads();
+  const KthKey k = kth_key(n, take, 56, st, [&](int i) { return score_key(exact[i]); });
+  int placed = 0, seen = 0;
+  for (int i0 = 0; i0 < n; i0 += kTokThreads) {
+    const int i = i0 + tid;
+    const unsigned long long key = i < n ? score_key(exact[i]) : 0ull;
+    const bool same = i < n && key == k.key;
+    int before, before_same, none, more, more_same;
+    count2(&fix->rank, same, false, &before_same, &none, &more_same, &none);
+    const bool mine = i < n && (key > k.key || (same && seen + before_same < k.equal));
+    count2(&fix->rank, mine, false, &before, &none, &more, &none);
+    if (mine) out[placed + before] = base + i;
+    placed += more;
+    seen += more_same;
+  }
 }
 
 // SEL: choose the blocks (idx, cnt are written). ATT: attend to them (with SEL to the chosen
@@ -293,7 +447,7 @@ __global__ void __launch_bounds__(kTokThreads)
   const int hk = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t row = static_cast<int64_t>(b) * p.hk + hk;  // (sequence, key head)
-  TokFixed* fix = reinterpret_cast<TokFixed*>(smem + p.union_bytes);
+  TokFixed* fix = reinterpret_cast<TokFixed*>(smem + p.fixed_at);
   uint64_t *full = fix->full, *empty = fix->empty;
   volatile uint32_t* abort_flag = &fix->abort_flag;
 
@@ -306,7 +460,7 @@ __global__ void __launch_bounds__(kTokThreads)
   const __nv_bfloat16* q = p.q + row * p.group * D;
   int32_t* list = p.idx + row * p.keep;
 
-  if (ATT && tid == 0) {
+  if (ATT && tid == 128) {  // the thread that loads
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 4);
@@ -318,27 +472,57 @@ __global__ void __launch_bounds__(kTokThreads)
   // Where the e-th kept block stands: every block (all), forced and chosen ones (few candidates,
   // ranked by every CTA), or the list that the first CTA wrote.
   const int n_cand = nb - p.n_sink - p.n_recent, take = p.keep - p.n_sink - p.n_recent;
-  const bool all = SEL && nb <= p.keep, few = SEL && !all && n_cand <= kTokThreads;
+  const bool all = SEL && nb <= p.keep, few = SEL && !all && n_cand <= kFew;
+  // The i-th entry of this CTA: with SEL the recent blocks come first, then the first ones, then the
+  // chosen ones.
+  auto entry = [&](int i) {
+    const int pos = rank + i * size;
+    if (!SEL || all) return pos;
+    return pos < p.n_recent ? p.keep - p.n_recent + pos : pos - p.n_recent;
+  };
+  auto load_tile = [&](uint32_t it, int j) {  // K (even it) or V of block j into its stage
+    const uint32_t st = it % C::kStages;
+    mbar_arrive_expect_tx(&full[st], C::kTileBytes);
+#pragma unroll
+    for (int c = 0; c < C::kChunks; ++c)
+      tma_load_3d(smem_u32(smem) + st * C::kTileBytes + c * C::kChunkBytes, (it & 1u) == 0 ? &tm_k : &tm_v, &full[st],
+                  c * 64, j * 128, static_cast<int>(row));
+  };
+  // Tiles that are loaded before the choice is made: of every block where all are kept, else of the
+  // forced ones, as far as the ring goes.
+  int early = 0;
+  if (SEL && ATT && p.score_at != 0) {
+    const int known = all ? nb : p.n_recent + p.n_sink;
+    early = known > rank ? 2 * ((known - rank + size - 1) / size) : 0;
+    if (early > C::kStages) early = C::kStages;
+    if (tid == 128)
+      for (int it = 0; it < early; ++it) {
+        const int e = entry(it >> 1);
+        load_tile(it, all || e < p.n_sink ? e : nb - p.keep + e);
+      }
+  }
   bool synced = false;
   if (SEL && !all && take > 0) {  // 0 < take < n_cand
     const float* means = p.means + (row * p.nb_cap + p.n_sink) * D;
     if (few) {
-      score_blocks<D>(q, p.group, means, n_cand, 0, kTokThreads / 8, fix->score);
+      score_fast<D>(q, p.group, means, n_cand, 0, kTokThreads / 8, fix->fast);
       __syncthreads();
-      rank_few(fix->score, n_cand, take, fix->chosen, fix->warp_tot);
+      rank_few<D>(fix, q, p.group, means, n_cand, take);
       __syncthreads();
     } else {
       if (size > 1) cluster.sync();  // the first CTA runs before anyone writes to it
       constexpr int kPer = kTokThreads / 8;  // blocks a CTA scores at a time
-      score_blocks<D>(q, p.group, means, n_cand, rank * kPer, size * kPer,
-                      cluster.map_shared_rank(reinterpret_cast<double*>(smem), 0));
+      score_fast<D>(q, p.group, means, n_cand, rank * kPer, size * kPer,
+                    cluster.map_shared_rank(reinterpret_cast<float2*>(smem + p.score_at), 0));
       if (size > 1)
         cluster.sync();
       else
         __syncthreads();
       if (rank == 0) {
-        RankState* st = reinterpret_cast<RankState*>(smem + ((static_cast<size_t>(n_cand) * 8 + 15) & ~15ull));
-        rank_and_write(reinterpret_cast<const double*>(smem), n_cand, take, p.n_sink, list + p.n_sink, st);
+        uint8_t* mine = smem + p.score_at;
+        RankState* st = reinterpret_cast<RankState*>(mine + ((static_cast<size_t>(n_cand) * 8 + 15) & ~15ull));
+        rank_many<D>(reinterpret_cast<float2*>(mine), fix, st, q, p.group, means, n_cand, take, p.n_sink,
+                     list + p.n_sink);
       }
       if (size > 1) {
         cluster.sync();  // the list is written
@@ -371,7 +555,7 @@ __global__ void __launch_bounds__(kTokThreads)
   const int n_mine = n_ent > rank ? (n_ent - rank + size - 1) / size : 0;
   // Block of this CTA's i-th entry, or -1 (recorded) where it names no block that holds tokens.
   auto block_at = [&](int i, bool report) {
-    const int e = rank + i * size;
+    const int e = entry(i);
     const int j = SEL && (all || few || e < p.n_sink || e >= p.keep - p.n_recent)
                       ? kept_at(e)
                       : *const_cast<volatile int32_t*>(list + e);
@@ -393,21 +577,18 @@ __global__ void __launch_bounds__(kTokThreads)
   if (warp == 4) {
     // ------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the scores lay where tiles go
+      if (early == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // scores may have lain there
       uint32_t it = 0;
       bool ok = true;
       for (int i = 0; ok && i < n_mine; ++i) {
         const int j = block_at(i, true);
         if (j < 0) continue;
         for (int kv = 0; kv < 2; ++kv, ++it) {
+          if (static_cast<int>(it) < early) continue;
           const uint32_t st = it % C::kStages;
           ok = mbar_wait(&empty[st], ((it / C::kStages) & 1u) ^ 1u, abort_flag, p.status);
           if (!ok) break;
-          mbar_arrive_expect_tx(&full[st], C::kTileBytes);
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            tma_load_3d(smem_u32(smem) + st * C::kTileBytes + c * C::kChunkBytes, kv == 0 ? &tm_k : &tm_v, &full[st],
-                        c * 64, j * 128, static_cast<int>(row));
+          load_tile(it, j);
         }
       }
       for (uint32_t st = 0; st < C::kStages; ++st)
@@ -645,25 +826,34 @@ __global__ void __launch_bounds__(256)
 std::mutex g_attr_mutex;
 bool g_attrs_set[kMaxDevices];
 
-uint32_t tok_union_bytes(int d, int64_t nb, bool sel, bool att) {
+constexpr uint32_t kScoreBeside = 10000;  // scores up to here get their own room: two CTAs an SM still fit
+
+// Shared memory: the ring, the scores of many candidates (behind the ring, or in its place), TokFixed.
+void tok_layout(int d, int64_t nb, bool many, bool att, uint32_t* score_at, uint32_t* fixed_at) {
   const uint32_t ring = att ? (d == 128 ? TokConfig<128>::kRingBytes : TokConfig<64>::kRingBytes) : 0;
-  const uint32_t rank = sel ? static_cast<uint32_t>(nb * 8 + 16 + sizeof(RankState)) : 0;
-  return ((ring > rank ? ring : rank) + 1023u) & ~1023u;
+  const uint32_t score = many ? static_cast<uint32_t>(nb * 8 + 16 + sizeof(RankState)) : 0;
+  const bool beside = score <= kScoreBeside;
+  *score_at = beside ? ring : 0;
+  *fixed_at = ((beside ? ring + score : ring > score ? ring : score) + 127u) & ~127u;
 }
 
 template <int D>
 int tok_set_attrs() {
-  const uint32_t most = tok_union_bytes(D, kTokMaxBlocks, true, true) + 1024 + sizeof(TokFixed);
+  uint32_t score_at, fixed_at;
+  tok_layout(D, kTokMaxBlocks, true, true, &score_at, &fixed_at);
+  const uint32_t most = fixed_at + 1024 + sizeof(TokFixed);
   for (auto kernel : {token_kernel<D, true, true>, token_kernel<D, true, false>, token_kernel<D, false, true>})
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
       return SPARSTAR_ERR_CUDA;
   return SPARSTAR_OK;
 }
 
-// CTAs of a cluster: enough to give every SM two CTAs, at most one per two kept blocks.
+// CTAs of a cluster: enough to give every SM about four CTAs (two at a time: the last ones then leave
+// little idle; 48 sequences x 8 key heads, 32 blocks of 64 KB: 124 us of attention with clusters of two,
+// 130 us with one, 129 us with four), at most one per two kept blocks.
 int tok_cluster(int n_seq, int heads_k, int keep, int sms) {
   int c = 1;
-  while (c < 8 && static_cast<int64_t>(n_seq) * heads_k * c < 2 * sms && 4 * c <= keep) c *= 2;
+  while (c < 8 && static_cast<int64_t>(n_seq) * heads_k * c < 4 * sms && 4 * c <= keep) c *= 2;
   return c;
 }
 
@@ -727,12 +917,13 @@ int token_run(bool sel, bool att, const void* q, const void* k, const void* v, c
   p.n_recent = n_recent;
   const float scale = sm_scale > 0.f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.union_bytes = tok_union_bytes(head_dim, p.nb_cap, sel && p.nb_cap > keep, att);
+  tok_layout(head_dim, p.nb_cap, sel && p.nb_cap - n_sink - n_recent > kFew && p.nb_cap > keep, att, &p.score_at,
+             &p.fixed_at);
   const unsigned c = static_cast<unsigned>(tok_cluster(n_seq, heads_k, keep, dev->sms));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, static_cast<unsigned>(heads_k), static_cast<unsigned>(n_seq));
   cfg.blockDim = dim3(kTokThreads);
-  cfg.dynamicSmemBytes = p.union_bytes + 1024 + sizeof(TokFixed);
+  cfg.dynamicSmemBytes = p.fixed_at + 1024 + sizeof(TokFixed);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
