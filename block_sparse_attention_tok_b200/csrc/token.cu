@@ -610,6 +610,13 @@ __global__ void __launch_bounds__(kTokThreads)
         const int r = g + 8 * (e & 1), c = 16 * kk + c2 + 8 * (e >> 1);
         qa[kk][e] = r < p.group ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D + c)) : 0u;
       }
+    // Gives a stage back. The proxy fence holds the arrival until this warp's ldmatrix reads are done:
+    // the copy that follows writes through the async proxy, and without the fence it overtook them.
+    auto release = [&](uint32_t st) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[st]);
+    };
     uint32_t it = 0;
     for (int i = 0; i < n_mine; ++i) {
       const int j = block_at(i, false);
@@ -635,8 +642,7 @@ __global__ void __launch_bounds__(kTokThreads)
           mma16816(s[nt], qa[2 * k2 + 1], kb[2], kb[3]);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      release(st);
       float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
@@ -694,8 +700,7 @@ __global__ void __launch_bounds__(kTokThreads)
           mma16816(acc[t + 1], pa[ks], vb[2] & keep_lo, vb[3] & keep_hi);
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[st]);
+      release(st);
     }
   }
   __syncthreads();  // the ring is free
