@@ -444,9 +444,9 @@ def attn_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor
         dv = torch.empty_like(v) if dv is None else dv
         if workspace is None:
             workspace = AttnBwdWorkspace(H, n_q, n_kv, d, kmax, q.device, block)
-        _check(load().sparstar_attn_bwd(_ptr(do), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), H, n_q, n_kv, d,
-                                        int(block), _ptr(idx), _ptr(cnt), kmax, float(sm_scale), _ptr(dq), _ptr(dk),
-                                        _ptr(dv), _ptr(workspace.buf), workspace.nbytes, st), "sparstar_attn_bwd")
+        _check(load().sparstar_attn_bwd(_at(do), _at(q), _at(k), _at(v), _at(o), _at(lse), H, n_q, n_kv, d,
+                                        int(block), _at(idx), _at(cnt), kmax, float(sm_scale), _at(dq), _at(dk),
+                                        _at(dv), _at(workspace.buf), workspace.nbytes, st), "sparstar_attn_bwd")
     return dq, dk, dv
 
 
@@ -468,7 +468,9 @@ class _launch:
             self.switched.enter_context(torch.cuda.device(self.device))
             if self.stream is not None:
                 self.switched.enter_context(torch.cuda.stream(self.stream))
-        return int((self.stream or torch.cuda.current_stream()).cuda_stream) or None
+                return self.stream.cuda_stream
+        # the pointer alone: a Stream object costs as much as everything else here
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.switched is not None:
@@ -485,6 +487,10 @@ def _check_device(device, *tensors):
 
 
 _NO_VIEW = View(None, 0, 0, 0)
+
+
+def _at(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _view(name: str, t: Optional[torch.Tensor], shape, dtype, token: int, head: int, seq: int = -1) -> View:
@@ -554,20 +560,20 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[
     _check_device(device, k, v, wq, wk, cos, sin, q_out, k_out, v_out, kv_rows)
     with _launch(device, stream) as st:
         if q_out is None:
-            q_out = torch.empty((hq, n, d), dtype=bf16, device=device)
+            q_out = q.new_empty((hq, n, d), dtype=bf16)
         if k is not None and k_out is None:
-            k_out = torch.empty((hk, kv_offset + n, d), dtype=bf16, device=device)
+            k_out = q.new_empty((hk, kv_offset + n, d), dtype=bf16)
         rows, kv_shape, dims = 0, None, (1, 0)
         if k_out is not None:
             rows, kv_shape = k_out.shape[-2], (hk, k_out.shape[-2], d)
             if kv_rows is not None and k_out.dim() == 4:
                 kv_shape, dims = (n, *kv_shape), (2, 1, 0)
         if v is not None and v_out is None:
-            v_out = torch.empty((hk, kv_offset + n, d) if kv_shape is None else kv_shape, dtype=bf16, device=device)
+            v_out = q.new_empty((hk, kv_offset + n, d) if kv_shape is None else kv_shape, dtype=bf16)
         _check(load().sparstar_qk_norm_rope(
-            qv, kv, vv, _X_DTYPES[x_dtype], n, hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, interleaved,
+            qv, kv, vv, _X_DTYPES[x_dtype], n, hq, hk, d, _at(wq), _at(wk), _at(cos), _at(sin), eps, interleaved,
             _view("q_out", q_out, (hq, n, d), bf16, 1, 0), _view("k_out", k_out, kv_shape, bf16, *dims),
-            _view("v_out", v_out, kv_shape, bf16, *dims), _ptr(kv_rows), kv_offset, rows, st), "sparstar_qk_norm_rope")
+            _view("v_out", v_out, kv_shape, bf16, *dims), _at(kv_rows), kv_offset, rows, st), "sparstar_qk_norm_rope")
     return q_out, k_out, v_out
 
 
@@ -599,17 +605,17 @@ def qk_norm_rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], q: torch.Tens
     _check_device(device, dq, dk, dv, k, wq, wk, cos, sin, dq_in, dk_in, dv_in)
     with _launch(device, stream) as st:
         if dq_in is None:
-            dq_in = torch.empty((n, hq, d), dtype=x_dtype, device=device)
+            dq_in = q.new_empty((n, hq, d))
         if dk is not None and dk_in is None:
-            dk_in = torch.empty((n, hk, d), dtype=x_dtype, device=device)
+            dk_in = q.new_empty((n, hk, d))
         if dv is not None and dv_in is None:
-            dv_in = torch.empty((n, hk, d), dtype=x_dtype, device=device)
-        dw = torch.empty((2, d), dtype=torch.float32, device=device)
+            dv_in = q.new_empty((n, hk, d))
+        dw = q.new_empty((2, d), dtype=torch.float32)
         nbytes = _norm_rope_bwd_workspace_size(d)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = q.new_empty(nbytes, dtype=torch.uint8)
         at = dw.data_ptr()
         _check(load().sparstar_qk_norm_rope_bwd(
-            *views, _X_DTYPES[x_dtype], n, hq, hk, d, _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin), eps, interleaved,
+            *views, _X_DTYPES[x_dtype], n, hq, hk, d, _at(wq), _at(wk), _at(cos), _at(sin), eps, interleaved,
             kv_offset, _view("dq_in", dq_in, (n, hq, d), x_dtype, 0, 1),
             _view("dk_in", dk_in, (n, hk, d), x_dtype, 0, 1), _view("dv_in", dv_in, (n, hk, d), x_dtype, 0, 1), at,
             at + 4 * d if dk is not None else None, ws.data_ptr(), nbytes, st), "sparstar_qk_norm_rope_bwd")
@@ -682,7 +688,7 @@ def block_means(k: torch.Tensor, kv_len: torch.Tensor, means: Optional[torch.Ten
     with _launch(k.device, stream) as st:
         if means is None:
             means = torch.zeros(b, hk, -(-s // BLOCK), d, dtype=torch.float32, device=k.device)
-        _check(load().sparstar_block_means(_ptr(k), _ptr(kv_len), b, hk, s, d, int(tail_only), _ptr(means), st),
+        _check(load().sparstar_block_means(_at(k), _at(kv_len), b, hk, s, d, int(tail_only), _at(means), st),
                "sparstar_block_means")
     return means
 
@@ -704,10 +710,10 @@ def token_select(q: torch.Tensor, means: torch.Tensor, kv_len: torch.Tensor, kee
     _check_lists(idx, cnt, b, hk, keep)
     _check_device(q.device, means, kv_len, idx, cnt)
     with _launch(q.device, stream) as st:
-        idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
-        cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt
-        _check(load().sparstar_token_select(_ptr(q), _ptr(means), _ptr(kv_len), b, q.shape[1], hk, nb * BLOCK, d, keep,
-                                            int(n_sink), int(n_recent), _ptr(idx), _ptr(cnt), st),
+        idx = q.new_empty((b, hk, max(keep, 0)), dtype=torch.int32) if idx is None else idx
+        cnt = q.new_empty((b, hk), dtype=torch.int32) if cnt is None else cnt
+        _check(load().sparstar_token_select(_at(q), _at(means), _at(kv_len), b, q.shape[1], hk, nb * BLOCK, d, keep,
+                                            int(n_sink), int(n_recent), _at(idx), _at(cnt), st),
                "sparstar_token_select")
     return idx, cnt
 
@@ -727,9 +733,9 @@ def token_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.
     with _launch(q.device, stream) as st:
         o = torch.empty_like(q) if o is None else o
         if want_lse and lse is None:
-            lse = torch.empty(b, q.shape[1], dtype=torch.float32, device=q.device)
-        _check(load().sparstar_token_attn(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), b, q.shape[1], hk, s, d, _ptr(idx),
-                                          _ptr(cnt), idx.shape[2], float(sm_scale), _ptr(o), _ptr(lse), st),
+            lse = q.new_empty((b, q.shape[1]), dtype=torch.float32)
+        _check(load().sparstar_token_attn(_at(q), _at(k), _at(v), _at(kv_len), b, q.shape[1], hk, s, d, _at(idx),
+                                          _at(cnt), idx.shape[2], float(sm_scale), _at(o), _at(lse), st),
                "sparstar_token_attn")
     return o, lse
 
@@ -745,14 +751,14 @@ def token_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: tor
     _check_token_out(o, lse, q)
     _check_device(q.device, idx, cnt, o, lse)
     with _launch(q.device, stream) as st:
-        idx = torch.empty(b, hk, max(keep, 0), dtype=torch.int32, device=q.device) if idx is None else idx
-        cnt = torch.empty(b, hk, dtype=torch.int32, device=q.device) if cnt is None else cnt
+        idx = q.new_empty((b, hk, max(keep, 0)), dtype=torch.int32) if idx is None else idx
+        cnt = q.new_empty((b, hk), dtype=torch.int32) if cnt is None else cnt
         o = torch.empty_like(q) if o is None else o
         if want_lse and lse is None:
-            lse = torch.empty(b, q.shape[1], dtype=torch.float32, device=q.device)
-        _check(load().sparstar_token_forward(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_len), _ptr(means), b, q.shape[1], hk,
-                                             s, d, keep, int(n_sink), int(n_recent), float(sm_scale), _ptr(idx),
-                                             _ptr(cnt), _ptr(o), _ptr(lse), st), "sparstar_token_forward")
+            lse = q.new_empty((b, q.shape[1]), dtype=torch.float32)
+        _check(load().sparstar_token_forward(_at(q), _at(k), _at(v), _at(kv_len), _at(means), b, q.shape[1], hk,
+                                             s, d, keep, int(n_sink), int(n_recent), float(sm_scale), _at(idx),
+                                             _at(cnt), _at(o), _at(lse), st), "sparstar_token_forward")
     return o, lse, idx, cnt
 
 
