@@ -176,7 +176,9 @@ __device__ KthKey kth_key(int n, int take, int shift, RankState* st, F&& key) {
 // scored again, in fp64, where neighbours need it. Scores that are not finite make E so, and every
 // block lies between. (48 sequences x 8 key heads, 297 candidates each: the selection alone takes 22 us,
 // with every score in fp64 36 us, most of it conversions of the means.)
-constexpr float kScoreMargin = 2.25f / 262144.f;  // 2E / max B, with room for the comparison's rounding
+// The margin 2E of a largest B, with room for the comparison's rounding and, where products fall below
+// the normal range, for the 2^-150 that each may lose there.
+__device__ __forceinline__ float score_margin(float most) { return most * (2.25f / 262144.f) + 1e-42f; }
 
 __device__ __forceinline__ uint32_t score_key32(float s) {
   if (isnan(s)) return 0u;
@@ -336,7 +338,7 @@ __device__ __forceinline__ void rank_few(TokFixed* fix, const __nv_bfloat16* q, 
   const float2 v = in ? fix->fast[tid] : make_float2(0.f, 0.f);
   const uint32_t key = in ? score_key32(v.x) : 0u;
   fix->key[tid] = key;
-  const float margin = max_over_cta(&fix->rank, v.y) * kScoreMargin;
+  const float margin = score_margin(max_over_cta(&fix->rank, v.y));
   int above = 0;
 #pragma unroll 8
   for (int i = 0; i < n; ++i) above += fix->key[i] + (i < tid ? 1u : 0u) > key;
@@ -372,7 +374,7 @@ __device__ void rank_many(float2* scores, TokFixed* fix, RankState* st, const __
   const int tid = threadIdx.x;
   float most = 0.f;
   for (int i = tid; i < n; i += kTokThreads) most = (isnan(most) || most > scores[i].y) ? most : scores[i].y;
-  const float margin = max_over_cta(&fix->rank, most) * kScoreMargin;
+  const float margin = score_margin(max_over_cta(&fix->rank, most));
   bool all_exact = !isfinite(margin);
   if (!all_exact) {
     const uint32_t cut_key = static_cast<uint32_t>(

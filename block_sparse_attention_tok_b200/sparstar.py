@@ -460,6 +460,8 @@ class _launch:
     __slots__ = ("device", "stream", "switched")
 
     def __init__(self, device: torch.device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
         self.device, self.stream, self.switched = device, stream, None
 
     def __enter__(self):

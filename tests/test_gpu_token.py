@@ -195,6 +195,18 @@ def test_scores_that_are_not_finite_among_others(S, n):
             assert idx[0, h].tolist() == want
 
 
+def test_scores_below_the_normal_range_still_rank(S):
+    g = torch.Generator().manual_seed(5)
+    for n in (100, 500):
+        values = (torch.randint(1, 2000, (n,), generator=g).double() * 2.0 ** -149).float()
+        means = torch.zeros(1, 1, n + 1, 64, device="cuda")
+        means[0, 0, :n, :4] = values[torch.randint(0, n, (n, 4), generator=g)].cuda()
+        q = torch.tensor([0.75, -0.5, 1.25, 0.3125] + [0.0] * 60).bfloat16().reshape(1, 1, 64).cuda()
+        kv_len = torch.tensor([(n + 1) * 128], dtype=torch.int32, device="cuda")
+        idx, _ = S.token_select(q, means, kv_len, n // 3, 0, 1)
+        assert idx[0, 0].tolist() == R.choose(q[0], means[0, 0], (n + 1) * 128, n // 3, 0, 1)
+
+
 def test_near_scores_are_told_apart_beyond_fp32(S):
     """Scores that differ by less than fp32 sums resolve still rank by their fp64 values."""
     means = torch.zeros(1, 1, 4, 64, device="cuda")
