@@ -95,10 +95,8 @@ struct BwdPhaseBars {
   uint64_t st_full[2], st_empty[2];  // lse and delta of the walked rows (dK/dV only)
   uint64_t held_full, held_empty;    // the held pair of tiles (K, V)
   uint64_t s_full[2], p_full;        // S ready / P written
-  uint64_t dp_full, dp_read;         // dP ready / dP taken into registers (dQ only)
-  // dS written. dQ uses both in turn: a warp may reach tile n + 1 (whose S and dP wait only for
-  // dP(n) to be read) before another has arrived for tile n, and must not be counted there.
-  uint64_t ds_full[2];
+  uint64_t dp_full, ds_full;         // dP ready / dS written
+  uint64_t hold_tm, s_read;          // Q and dO in tensor memory / S taken into registers (dQ only)
   uint64_t acc_full;
 };
 
@@ -124,13 +122,14 @@ __device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
       mbar_init(&b->st_full[i], 1);
       mbar_init(&b->st_empty[i], 1);
       mbar_init(&b->s_full[i], 1);
-      mbar_init(&b->ds_full[i], 8);
     }
     mbar_init(&b->held_full, 1);
-    mbar_init(&b->held_empty, 1);
+    mbar_init(&b->held_empty, b == &bars->dkv ? 1 : 8);  // by the products, or by the warps that copy it
     mbar_init(&b->p_full, 8);  // one arrival per softmax warp, here and below
     mbar_init(&b->dp_full, 1);
-    mbar_init(&b->dp_read, 8);
+    mbar_init(&b->ds_full, 8);
+    mbar_init(&b->hold_tm, 8);
+    mbar_init(&b->s_read, 8);
     mbar_init(&b->acc_full, 1);
   }
   for (int i = 0; i < 2; ++i) {
@@ -223,10 +222,13 @@ __device__ __forceinline__ void bwd_store_row(uint32_t taddr, __nv_bfloat16* dst
 // dP(n+1) run, so S, dP and the two accumulators need one buffer each (all 512 columns).
 // S(n+1) may overwrite P(n): tcgen05.mma of one thread run in order.
 //
-// dQ. Tensor memory: S of even and odd tiles [0,128), [128,256), dP [256,384), dQ [384,384+D): rows
-// are query tokens. Issue order per tile n: S(n+1) = Q K(n+1)^T; dP(n+1) = dO V(n+1)^T once dP(n) is
-// in registers; dQ += dS(n) K(n), with dS(n) over S(n). The softmax warps never wait for a product
-// that starts after their own previous step.
+// dQ. Tensor memory: S [0,128), dP [128,256), Q and dO as bf16 pairs [256,256+D), dQ [384,384+D): rows
+// are query tokens. Issue order per tile n:
+//   S(n+1) = Q K(n+1)^T once S(n) is in registers;  dQ += dS(n) K(n);  dP(n+1) = dO V(n+1)^T,
+// with dS(n) over dP(n), in its halves' own columns. The exponentials of tile n+1 run beside dQ(n) and
+// dP(n+1). Q and dO are operands of every tile: from tensor memory they cost no shared-memory
+// bandwidth, which a product with both operands in shared memory takes whole (128 bytes a cycle) while
+// the tiles' copies need a share of it (FIGURE).
 //
 // Between the two a CTA hands its shared memory over when its last dK/dV product is done and its
 // tensor memory when the last dV and dK rows have been read.
@@ -266,7 +268,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
   const uint32_t tmem = bars->tmem;
   griddep_wait();  // row statistics, lists and the item counter come from the kernels before
   constexpr uint32_t kS = 0, kDPk = 128, kDV = 256, kDK = 384;  // dK, dV items
-  constexpr uint32_t kDPq = 256, kDQ = 384;                     // dQ items
+  constexpr uint32_t kDPq = 128, kQ = 256, kDO = 256 + D / 2, kDQ = 384;  // dQ items
 
   auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, p.status));
@@ -452,26 +454,28 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         __syncwarp();
         return true;
       };
+      auto product_t = [&](uint32_t d, uint32_t a, uint64_t b) {  // the same, A in tensor memory
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ts(d, a + 8 * kk, b + (((kk >> 2) * C::kChunkBytes + (kk & 3) * 32) >> 4), C::kIdescS, kk > 0 ? 1u : 0u);
+      };
       auto q_issue_s = [&](uint32_t u) -> bool {
         const uint32_t sa = u % C::kStagesA;
         if (!wait_all(&bq->a_full[sa], (u / C::kStagesA) & 1u)) return false;
         if (elect_one()) {
-          product(tmem + kS + 128u * (u & 1u), h0, ra + stage_of(sa));
-          mma_commit(&bq->s_full[u & 1u]);
+          product_t(tmem + kS, tmem + kQ, ra + stage_of(sa));
+          mma_commit(&bq->s_full[0]);
         }
         __syncwarp();
         return true;
       };
-      auto q_issue_dp = [&](uint32_t u, bool last) -> bool {
+      auto q_issue_dp = [&](uint32_t u) -> bool {
         const uint32_t sb = u % C::kStagesB;
-        if (u > 0 && !wait_all(&bq->dp_read, (u - 1) & 1u)) return false;
         if (!wait_all(&bq->b_full[sb], (u / C::kStagesB) & 1u)) return false;
-        tc_fence_after();
         if (elect_one()) {
-          product(tmem + kDPq, h1, rb + stage_of(sb));
+          product_t(tmem + kDPq, tmem + kDO, rb + stage_of(sb));
           mma_commit(&bq->dp_full);
           mma_commit(&bq->b_empty[sb]);
-          if (last) mma_commit(&bq->held_empty);
         }
         __syncwarp();
         return true;
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
             }
             __syncwarp();
             if (!last && !(ok = k_issue_s(tk + 1))) break;
-            if (!(ok = wait_all(&bk->ds_full[0], tk & 1u))) break;
+            if (!(ok = wait_all(&bk->ds_full, tk & 1u))) break;
             tc_fence_after();
             if (elect_one()) {
               gather(tmem + kDK, tmem + kDPk, ra_mn + stage_of(sa), n > 0);
@@ -515,21 +519,27 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
             if (!(ok = wait_all(&bars->tmem_free, 0u))) break;
             tc_fence_after();
           }
-          if (!(ok = wait_all(&bq->held_full, hq & 1u))) break;
+          if (!(ok = wait_all(&bq->hold_tm, hq & 1u))) break;
           ++hq;
-          ok = q_issue_s(tq) && q_issue_dp(tq, n_tiles == 1);
+          tc_fence_after();
+          ok = q_issue_s(tq) && q_issue_dp(tq);
           for (int n = 0; ok && n < n_tiles; ++n, ++tq) {
             const bool last = n == n_tiles - 1;
-            if (!last && !(ok = q_issue_s(tq + 1) && q_issue_dp(tq + 1, n == n_tiles - 2))) break;
-            if (!(ok = wait_all(&bq->ds_full[tq & 1u], (tq >> 1) & 1u))) break;
+            if (!last) {
+              if (!(ok = wait_all(&bq->s_read, tq & 1u))) break;
+              tc_fence_after();
+              if (!(ok = q_issue_s(tq + 1))) break;
+            }
+            if (!(ok = wait_all(&bq->ds_full, tq & 1u))) break;
             tc_fence_after();
             if (elect_one()) {
               const uint32_t sa = tq % C::kStagesA;
-              gather(tmem + kDQ, tmem + kS + 128u * (tq & 1u), ra_mn + stage_of(sa), n > 0);
+              gather(tmem + kDQ, tmem + kDPq, ra_mn + stage_of(sa), n > 0);
               mma_commit(&bq->a_empty[sa]);
               if (last) mma_commit(&bq->acc_full);
             }
             __syncwarp();
+            if (!last && !(ok = q_issue_dp(tq + 1))) break;
           }
         }
       }
@@ -555,7 +565,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
     const bool idle = B < 128 && wq * 32 >= B;
     const bool ragged_kv = p.n_kv % B != 0;
     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t tk = 0, tq = 0, dk_done = 0, dq_done = 0;
+    uint32_t tk = 0, tq = 0, hq = 0, dk_done = 0, dq_done = 0;
     bool ok = true, in_dq = false;
     for (uint32_t k = 0; ok; ++k) {
       int item, n_ent;
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (idle) {
             arrive(&bk->p_full);
             if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
-            arrive(&bk->ds_full[0]);
+            arrive(&bk->ds_full);
             continue;
           }
           tc_fence_after();
@@ -612,7 +622,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           }
           bwd_store_half(t_dp, pr);
           tmem_wait_st();
-          arrive(&bk->ds_full[0]);
+          arrive(&bk->ds_full);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bk->acc_full, dk_done & 1u))) break;
@@ -625,6 +635,8 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         if (!in_dq) {
           in_dq = true;
           arrive(&bars->tmem_free);
+          if (!(ok = wait_all(&bars->tmem_free, 0u))) break;  // Q and dO go where others read dV
+          tc_fence_after();
         }
         const int32_t* list = p.idx + static_cast<int64_t>(iq) * p.kmax;
         const int64_t tok = static_cast<int64_t>(blk) * B + row;
@@ -634,9 +646,29 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           neg_lse.x = neg_lse.y = __ldg(p.neg_lse2 + at);
           neg_delta.x = neg_delta.y = __ldg(p.neg_delta + at);
         }
+        // Q (first half of the warps) and dO (second half) from shared to tensor memory, a row a thread.
+        // The products of the item before have read the old ones: its accumulator was waited for.
+        if (!(ok = wait_all(&bq->held_full, hq & 1u))) break;
+        ++hq;
+        if (!idle) {
+          const uint8_t* src = (half == 0 ? held0 : held1) + row * 128;
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c) {
+            uint32_t w[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint4 x = *reinterpret_cast<const uint4*>(src + c * C::kChunkBytes + ((u ^ (row & 7)) << 4));
+              w[4 * u] = x.x, w[4 * u + 1] = x.y, w[4 * u + 2] = x.z, w[4 * u + 3] = x.w;
+            }
+            tmem_st32(tmem + lane_off + (half == 0 ? kQ : kDO) + 32 * c, w);
+          }
+          tmem_wait_st();
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // reads are done before the next copy lands
+        arrive(&bq->held_empty);
+        arrive(&bq->hold_tm);
+        const uint32_t t_s = tmem + lane_off + kS + 64 * half, t_dp = tmem + lane_off + kDPq + 64 * half;
         for (int n = 0; n < n_tiles; ++n, ++tq) {
-          const uint32_t t_s = tmem + lane_off + kS + 128u * (tq & 1u) + 64 * half;
-          const uint32_t t_dp = tmem + lane_off + kDPq + 64 * half;
           // valid columns of this half of the tile
           int nv = 64;
           if (BPT > 1 && half == 1 && 2 * n + 1 >= n_ent) nv = 0;  // odd last entry: its half repeats a block
@@ -647,17 +679,18 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
               nv = left < 0 ? 0 : left < 64 ? static_cast<int>(left) : 64;
             }
           }
-          if (!(ok = wait_all(&bq->s_full[tq & 1u], (tq >> 1) & 1u))) break;
+          if (!(ok = wait_all(&bq->s_full[0], tq & 1u))) break;
           if (idle) {
+            arrive(&bq->s_read);
             if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
-            arrive(&bq->dp_read);
-            arrive(&bq->ds_full[tq & 1u]);
+            arrive(&bq->ds_full);
             continue;
           }
           tc_fence_after();
           uint32_t r[2][32];
           float2 pr[32];
           bwd_load_half(t_s, r);
+          arrive(&bq->s_read);
 #pragma unroll
           for (int e = 0; e < 32; ++e) pr[e] = bwd_exp(bwd_pair(r, e), scale2, neg_lse);
           if (nv < 64) {
@@ -670,12 +703,11 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
           tc_fence_after();
           bwd_load_half(t_dp, r);
-          arrive(&bq->dp_read);
 #pragma unroll
           for (int e = 0; e < 32; ++e) pr[e] = __fmul2_rn(pr[e], __fadd2_rn(bwd_pair(r, e), neg_delta));
-          bwd_store_half(t_s, pr);
+          bwd_store_half(t_dp, pr);
           tmem_wait_st();
-          arrive(&bq->ds_full[tq & 1u]);
+          arrive(&bq->ds_full);
         }
         if (!ok) break;
         if (!(ok = wait_all(&bq->acc_full, dq_done & 1u))) break;
