@@ -43,10 +43,9 @@ struct BwdConfig {
   static constexpr int kStagesStat = 2;
   static constexpr uint32_t kStatBytes = 2 * 128 * 4;  // lse and delta of 128 query rows
   static constexpr int kThreads = 384;
-  static constexpr int kSoftmaxThreads = 256;
   static constexpr int kLoadWarp = 8;
   static constexpr int kMmaWarp = 9;
-  static constexpr int kRegsSoftmax = 208, kRegsProducer = 80;
+  static constexpr int kRegsSoftmax = 200, kRegsProducer = 96;
   static constexpr int kRegsNeeded = 256 * kRegsSoftmax + 128 * kRegsProducer;
   static constexpr int kLaunchRegs = (65536 / kThreads) & ~7;
   static_assert(kRegsNeeded <= kThreads * kLaunchRegs, "setmaxnreg split above the launch allocation");
@@ -94,7 +93,7 @@ struct BwdPhaseBars {
   uint64_t b_full[2], b_empty[2];    // the other walked operand (dO)
   uint64_t st_full[2], st_empty[2];  // lse and delta of the walked rows (dK/dV only)
   uint64_t held_full, held_empty;    // the held pair of tiles (K, V)
-  uint64_t s_full[2], p_full;        // S ready / P written
+  uint64_t s_full, p_full;           // S ready / P written (dK/dV only)
   uint64_t dp_full, ds_full;         // dP ready / dS written
   uint64_t hold_tm, s_read;          // Q and dO in tensor memory / S taken into registers (dQ only)
   uint64_t acc_full;
@@ -121,8 +120,8 @@ __device__ __forceinline__ void bwd_bars_init(BwdBars* bars) {
       mbar_init(&b->b_empty[i], 1);
       mbar_init(&b->st_full[i], 1);
       mbar_init(&b->st_empty[i], 1);
-      mbar_init(&b->s_full[i], 1);
     }
+    mbar_init(&b->s_full, 1);
     mbar_init(&b->held_full, 1);
     mbar_init(&b->held_empty, b == &bars->dkv ? 1 : 8);  // by the products, or by the warps that copy it
     mbar_init(&b->p_full, 8);  // one arrival per softmax warp, here and below
@@ -228,7 +227,10 @@ __device__ __forceinline__ void bwd_store_row(uint32_t taddr, __nv_bfloat16* dst
 // with dS(n) over dP(n), in its halves' own columns. The exponentials of tile n+1 run beside dQ(n) and
 // dP(n+1). Q and dO are operands of every tile: from tensor memory they cost no shared-memory
 // bandwidth, which a product with both operands in shared memory takes whole (128 bytes a cycle) while
-// the tiles' copies need a share of it (FIGURE).
+// the tiles' copies need a share of it. Four heads of the 720p final scale, back to back at the power
+// cap: 5.98 ms, with Q and dO read from shared memory 6.16 ms. K and V of the dK/dV items find no room
+// there beside two accumulators; steps of 64 query rows would make it, but their barriers cost more
+// (6.32 ms against 5.91 ms on the same GPU).
 //
 // Between the two a CTA hands its shared memory over when its last dK/dV product is done and its
 // tensor memory when the last dV and dK rows have been read.
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
       if (lane == 0) {
         const uint64_t pol_held = l2_policy_evict_first(), pol_walk = l2_policy_evict_last();
         uint32_t tk = 0, tq = 0, hk = 0, hq = 0;  // tiles and held pairs loaded in either phase
-        // A tile of one operand: `row[b]` is the first row of each of its boxes.
+        // A tile of one operand, from the blocks blk[0..BPT).
         auto load_tile = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, const int (&blk)[BPT], int h) {
           mbar_arrive_expect_tx(bar, TB);
 #pragma unroll
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         if (!wait_all(&bk->a_full[sa], (u / C::kStagesA) & 1u)) return false;
         if (elect_one()) {
           product(tmem + kS, h0, ra + stage_of(sa));
-          mma_commit(&bk->s_full[0]);
+          mma_commit(&bk->s_full);
         }
         __syncwarp();
         return true;
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
         if (!wait_all(&bq->a_full[sa], (u / C::kStagesA) & 1u)) return false;
         if (elect_one()) {
           product_t(tmem + kS, tmem + kQ, ra + stage_of(sa));
-          mma_commit(&bq->s_full[0]);
+          mma_commit(&bq->s_full);
         }
         __syncwarp();
         return true;
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
           const float4* lse = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + half * 256);
           const float4* del = reinterpret_cast<const float4*>(st_ring + sb * C::kStatBytes + 512 + half * 256);
           if (!(ok = wait_all(&bk->st_full[sb], (tk >> 1) & 1u))) break;
-          if (!(ok = wait_all(&bk->s_full[0], tk & 1u))) break;
+          if (!(ok = wait_all(&bk->s_full, tk & 1u))) break;
           if (idle) {
             arrive(&bk->p_full);
             if (!(ok = wait_all(&bk->dp_full, tk & 1u))) break;
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
               nv = left < 0 ? 0 : left < 64 ? static_cast<int>(left) : 64;
             }
           }
-          if (!(ok = wait_all(&bq->s_full[0], tq & 1u))) break;
+          if (!(ok = wait_all(&bq->s_full, tq & 1u))) break;
           if (idle) {
             arrive(&bq->s_read);
             if (!(ok = wait_all(&bq->dp_full, tq & 1u))) break;
