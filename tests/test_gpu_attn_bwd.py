@@ -233,6 +233,51 @@ def test_no_queries_give_zero_gradients(S):
     assert dq.shape == q.shape and (dk == 0).all() and (dv == 0).all()
 
 
+def test_the_largest_number_of_kv_blocks(S):
+    n_q, n_kv, d, block = 100, 49152 * 64 - 3, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(40)
+    k, v = (torch.randn(1, n_kv, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    q, do = (torch.randn(1, n_q, d, generator=g, device="cuda").bfloat16() for _ in range(2))
+    idx = torch.tensor([[[49151, 0, 30000], [7, 49151, 20000]]], dtype=torch.int32, device="cuda")
+    cnt = torch.tensor([[3, 2]], dtype=torch.int32, device="cuda")
+    o, lse = S.attn(q, k, v, idx, cnt, block=block)
+    dq, dk, dv = S.attn_bwd(do, q, k, v, o, lse, idx, cnt, block=block)
+    assert S.device_status() == S.OK
+    used = torch.tensor([0, 7, 30000, 49151], device="cuda")
+    rows = (used[:, None] * block + torch.arange(block, device="cuda")).flatten()
+    rows = rows[rows < n_kv]
+    w = torch.zeros(n_q, rows.numel(), dtype=torch.float64, device="cuda")
+    for i, keep in enumerate(([49151, 0, 30000], [7, 49151])):
+        for j in keep:
+            w[i * block:(i + 1) * block, rows // block == j] = 1
+    ref = R.head_backward(*(t[0].double() for t in (do, q)), k[0, rows].double(), v[0, rows].double(), o[0].double(),
+                          lse[0].double(), w, 1 / 8)
+    for x, (val, tol, _) in zip((dq[0], dk[0, rows], dv[0, rows]), ref):
+        assert ((x.double() - val).abs() <= tol).all()
+    for x in (dk, dv):
+        x[0, rows] = 0
+        assert not x.any()
+
+
+def test_two_calls_at_once(S):
+    """Two shapes on two streams, each with its own workspace, many times over."""
+    cases = []
+    for i, (n_q, n_kv, d, block) in enumerate(((700, 1500, 128, 128), (500, 900, 64, 64))):
+        q, k, v, do = inputs(2, n_q, n_kv, d, 30 + i)
+        idx, cnt = random_lists(2, n_q, n_kv, block, 30 + i)
+        o, lse = S.attn(q, k, v, idx, cnt, block=block)
+        args = (do, q, k, v, o, lse, idx, cnt)
+        cases.append((args, block, [t.clone() for t in S.attn_bwd(*args, block=block)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        for args, block, want, stream in cases:
+            got.append((S.attn_bwd(*args, block=block, stream=stream), want))
+    torch.cuda.synchronize()
+    assert S.device_status() == S.OK
+    assert all(torch.equal(a, b) for g, w in got for a, b in zip(g, w))
+
+
 def test_on_a_side_stream_and_in_a_graph(S):
     q, k, v, do = inputs(2, 500, 900, 128, 18)
     idx, cnt = random_lists(2, 500, 900, 128, 18)
