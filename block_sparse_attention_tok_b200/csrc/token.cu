@@ -926,7 +926,9 @@ int token_run(bool sel, bool att, const void* q, const void* k, const void* v, c
   p.scale_log2 = scale * 1.4426950408889634f;
   tok_layout(head_dim, p.nb_cap, sel && p.nb_cap - n_sink - n_recent > kFew && p.nb_cap > keep, att, &p.score_at,
              &p.fixed_at);
-  const unsigned c = static_cast<unsigned>(tok_cluster(n_seq, heads_k, keep, dev->sms));
+  // Without the attention, CTAs that would all rank the same few candidates are not worth a cluster.
+  const bool few = p.nb_cap - n_sink - n_recent <= kFew;
+  const unsigned c = !att && few ? 1u : static_cast<unsigned>(tok_cluster(n_seq, heads_k, keep, dev->sms));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(c, static_cast<unsigned>(heads_k), static_cast<unsigned>(n_seq));
   cfg.blockDim = dim3(kTokThreads);
