@@ -494,7 +494,8 @@ int sparstar_qk_norm_rope(sparstar_view q, sparstar_view k, sparstar_view v, int
   p.status = dev->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Four heads per item keep 64 bytes in flight per lane; with few tokens one head per item
-  // spreads the call over more SMs instead.
+  // spreads the call over more SMs instead (48 heads of 128 in bf16, four against one: 16 tokens 2.24
+  // and 1.96 us, 256 tokens 2.90 and 2.83 us, 512 tokens 3.49 and 4.20 us; fp32 crosses there too).
   nr_chunks(&p, 4);
   const bool wide = nr_items(p, head_dim) >= 2 * dev->sms;
   if (!wide) nr_chunks(&p, 1);

@@ -38,7 +38,9 @@ constexpr int kTokThreads = 160;      // 4 product warps and a TMA warp
 constexpr int kTokMaxGroup = 16;      // query heads of one key head
 constexpr int kTokMaxBlocks = 16384;  // blocks of one sequence whose scores fit shared memory
 constexpr int kDigitBins = 256;       // radix select: 8 bits a pass
-constexpr int kFew = kTokThreads;     // candidates that are ranked by counting, one a thread
+// Candidates that every CTA ranks for itself by counting, one a thread. With two a thread (up to 320) the
+// batch of 48 sequences x 8 key heads with up to 253 took 143 us, so 140 us.
+constexpr int kFew = kTokThreads;
 
 template <int D>
 struct TokConfig {
