@@ -42,16 +42,34 @@ int set_kernel_attrs(const DeviceInfo* dev) {
   return SPARSTAR_OK;
 }
 
+// Entries of a part of a list: an SM's share of all entries, so that no list holds a CTA longer than the
+// others work, but enough tiles to be worth the sums that a part stores. A list of n > part entries makes
+// ceil(n / part) < 2 n / part parts: with entries / 148 <= part, below 296 in all.
+int64_t bwd_part_entries(int heads, int64_t nqb, int32_t kmax) {
+  const int64_t share = (static_cast<int64_t>(heads) * nqb * kmax + 147) / 148;
+  return share < 16 ? 16 : share;
+}
+
+// Parts at most: none where no list (of nqb entries, or more only with blocks listed twice) can be that long.
+int bwd_parts(int heads, int64_t nqb, int32_t kmax) {
+  const int64_t part = bwd_part_entries(heads, nqb, kmax), all = static_cast<int64_t>(heads) * nqb * kmax;
+  const int64_t most = nqb * kmax <= part ? 0 : 2 * all / part;
+  return static_cast<int>(most < kBwdMaxParts ? most : kBwdMaxParts);
+}
+
 struct BwdWorkspace {
-  size_t next, lse2, delta, words, place, twice, col_at, col_row, total;
+  size_t next, done, parts, sums, lse2, delta, words, place, twice, col_at, col_row, total;
 };
 
-BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t kmax) {
+BwdWorkspace bwd_layout(int heads, int64_t nqb, int64_t nkb, int block, int32_t kmax, int head_dim) {
   const size_t h = static_cast<size_t>(heads);
   const size_t rows = align256(h * nqb * block * 4);
   BwdWorkspace w;
   w.next = 0;
-  w.lse2 = 256;
+  w.done = 256;
+  w.parts = w.done + align256(kBwdMaxParts * 8 * 4);
+  w.sums = w.parts + align256(kBwdMaxParts * sizeof(BwdPart));
+  w.lse2 = w.sums + static_cast<size_t>(bwd_parts(heads, nqb, kmax)) * 2 * block * head_dim * 4;
   w.delta = w.lse2 + rows;
   const size_t chunks = static_cast<size_t>((nqb + kMaskRows - 1) / kMaskRows);
   w.words = w.delta + rows;
@@ -95,7 +113,7 @@ int sparstar_attn_bwd_workspace_size(int heads, int64_t n_q, int64_t n_kv, int h
   if (bytes == nullptr) return SPARSTAR_ERR_ARG;
   const int rc = bwd_sizes(heads, n_q, n_kv, head_dim, block, kmax);
   if (rc != SPARSTAR_OK) return rc;
-  *bytes = bwd_layout(heads, ceil_blocks(n_q, block), ceil_blocks(n_kv, block), block, kmax).total;
+  *bytes = bwd_layout(heads, ceil_blocks(n_q, block), ceil_blocks(n_kv, block), block, kmax, head_dim).total;
   return SPARSTAR_OK;
 }
 
@@ -115,7 +133,7 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
       return SPARSTAR_ERR_ARG;
   }
   const int64_t nqb = ceil_blocks(n_q, block), nkb = ceil_blocks(n_kv, block);
-  const BwdWorkspace ws = bwd_layout(heads, nqb, nkb, block, kmax);
+  const BwdWorkspace ws = bwd_layout(heads, nqb, nkb, block, kmax, head_dim);
   if (n_q > 0 && (workspace == nullptr || workspace_bytes < ws.total ||
                   (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return SPARSTAR_ERR_WORKSPACE;
@@ -152,6 +170,10 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   r.twice = reinterpret_cast<int32_t*>(w + ws.twice);
   r.col_at = reinterpret_cast<int32_t*>(w + ws.col_at);
   r.col_row = reinterpret_cast<int32_t*>(w + ws.col_row);
+  r.parts = reinterpret_cast<BwdPart*>(w + ws.parts);
+  r.part_done = reinterpret_cast<int*>(w + ws.done);
+  const int64_t part = bwd_part_entries(heads, nqb, kmax);
+  r.part_ent = static_cast<int>(part < INT32_MAX ? part : INT32_MAX);
   r.next = reinterpret_cast<int*>(w + ws.next);
   r.status = dev->status;
   r.n_q = n_q;
@@ -173,6 +195,10 @@ int sparstar_attn_bwd(const void* d_o, const void* q, const void* k, const void*
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.status = dev->status;
   p.next = r.next;
+  p.parts = r.parts;
+  p.part_done = r.part_done;
+  p.part_sum = reinterpret_cast<float*>(w + ws.sums);
+  p.part_ent = r.part_ent;
   p.n_q = n_q;
   p.n_kv = n_kv;
   p.nqb = r.nqb;

@@ -37,7 +37,9 @@ def test_workspace_size(heads, n_q, n_kv, block, kmax):
         return (x + 255) // 256 * 256
     nqb, nkb = -(-n_q // block), -(-n_kv // block)
     chunks = -(-nqb // 32)
-    want = (256 + 2 * al(heads * nqb * block * 4) + 2 * al(heads * chunks * nkb * 4) + al(heads * chunks * 4)
+    share = max(16, -(-heads * nqb * kmax // 148))      # entries of a part of a long list
+    parts = 0 if nqb * kmax <= share else min(2 * heads * nqb * kmax // share, 296)
+    want = (256 + al(296 * 8 * 4) + al(296 * 20) + parts * 2 * block * 128 * 4 + 2 * al(heads * nqb * block * 4) + 2 * al(heads * chunks * nkb * 4) + al(heads * chunks * 4)
             + al(heads * (nkb + 1) * 4) + al(heads * nqb * kmax * 4))
     assert S.attn_bwd_workspace_size(heads, n_q, n_kv, 128, kmax, block) == want
     with pytest.raises(S.SparstarError):

@@ -90,6 +90,25 @@ def test_blocks_that_no_query_keeps_get_zero(S, block):
         assert (dk[h][~kept] == 0).all() and (dv[h][~kept] == 0).all()
 
 
+@pytest.mark.parametrize("block", [128, 64])
+@pytest.mark.parametrize("d", [64, 128])
+def test_lists_split_into_parts(S, d, block):
+    """One head whose ragged last block every query block keeps, another one that they keep twice, and
+    blocks that few keep: the long lists are split, and the parts added up the same way every time."""
+    n_q, n_kv = 130 * block + 7, 12 * block - 30
+    q, k, v, do = inputs(1, n_q, n_kv, d, 22)
+    nqb = -(-n_q // block)
+    g = torch.Generator().manual_seed(22)
+    idx = torch.stack([torch.tensor([11, 3, int(torch.randint(4, 11, (1,), generator=g)), 3]) for _ in range(nqb)])
+    idx = idx.to(torch.int32)[None].cuda().contiguous()
+    cnt = torch.full((1, nqb), 4, dtype=torch.int32, device="cuda")
+    o, lse = S.attn(q, k, v, idx, cnt, block=block)
+    want = check(S, do, q, k, v, idx, cnt, block, o=o, lse=lse)
+    for _ in range(5):
+        got = S.attn_bwd(do, q, k, v, o, lse, idx, cnt, block=block)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_every_block_kept_by_every_query(S):
     q, k, v, do = inputs(2, 700, 900, 128, 10)
     nqb, nkb = 6, 8
