@@ -16,8 +16,8 @@
 // One persistent kernel does both, one CTA per SM: 8 softmax warps (two per TMEM lane quarter,
 // each pair splitting the 128 columns of a tile), a TMA warp, an MMA warp. A thread keeps half a
 // row of P in fp32 registers between the two halves of its work (P from S, dS from dP).
-// P and dS are rounded to bf16 as operands of the tensor cores (half a step, 2^-9 of the value
-// on average, as the forward pass rounds P); all sums are fp32.
+// P and dS are rounded to bf16 as operands of the tensor cores (each off by at most 2^-8 of its
+// value, as the forward pass rounds P); all sums are fp32.
 #pragma once
 
 #include <cstdint>

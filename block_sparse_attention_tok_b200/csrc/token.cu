@@ -742,13 +742,12 @@ __global__ void __launch_bounds__(kTokThreads)
 #pragma unroll
     for (int w = 0; w < 4; ++w) m = fmaxf(m, pm[w * 16 + r]);
     float v = 0.f, l = 0.f;
-    if (m != -INFINITY) {
+    const float base = m == -INFINITY ? 0.f : m;  // no token, or scores that are NaN: l tells them apart
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = ex2_approx(pm[w * 16 + r] - m);
-        v = fmaf(f, po[(w * 16 + r) * kPad + c], v);
-        l = fmaf(f, pl[w * 16 + r], l);
-      }
+    for (int w = 0; w < 4; ++w) {
+      const float f = ex2_approx(pm[w * 16 + r] - base);
+      v = fmaf(f, po[(w * 16 + r) * kPad + c], v);
+      l = fmaf(f, pl[w * 16 + r], l);
     }
     co[i] = v;
     if (c == 0) {
@@ -765,16 +764,16 @@ __global__ void __launch_bounds__(kTokThreads)
     float m = -INFINITY;
     for (int x = 0; x < size; ++x) m = fmaxf(m, cluster.map_shared_rank(cm, x)[r]);
     float v = 0.f, l = 0.f;
-    if (m != -INFINITY)
-      for (int x = 0; x < size; ++x) {
-        const float f = ex2_approx(cluster.map_shared_rank(cm, x)[r] - m);
-        v = fmaf(f, cluster.map_shared_rank(co, x)[i], v);
-        l = fmaf(f, cluster.map_shared_rank(cl, x)[r], l);
-      }
+    const float base = m == -INFINITY ? 0.f : m;
+    for (int x = 0; x < size; ++x) {
+      const float f = ex2_approx(cluster.map_shared_rank(cm, x)[r] - base);
+      v = fmaf(f, cluster.map_shared_rank(co, x)[i], v);
+      l = fmaf(f, cluster.map_shared_rank(cl, x)[r], l);
+    }
     // a sequence with no kept token: o = 0, lse = -inf
-    p.o[row * p.group * D + i] = __float2bfloat16_rn(m == -INFINITY ? 0.f : v / l);
+    p.o[row * p.group * D + i] = __float2bfloat16_rn(l == 0.f ? 0.f : v / l);
     if (c == 0 && p.lse != nullptr)
-      p.lse[row * p.group + r] = m == -INFINITY ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      p.lse[row * p.group + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
   if (size > 1) cluster.sync();  // nobody leaves while its rows are read
 }

@@ -340,3 +340,27 @@ def test_no_sequences(S):
     means = S.block_means(k, kv_len)
     o, lse, idx, cnt = S.token_forward(q, k, k, kv_len, means, 4)
     assert o.shape == (0, 4, 64) and idx.shape == (0, 2, 4)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hk", [1, 160])  # clusters of several CTAs, and CTAs alone
+def test_a_nan_query_head_gives_nan_and_leaves_the_others(S, d, hk):
+    group, lens = 4, [700, 128, 0, 1, 1000]
+    q, k, v, kl = make(lens, group * hk, hk, 1024, d, 21)
+    cnt = ((kl + 127) // 128)[:, None].expand(-1, hk).contiguous()
+    idx = torch.arange(8, dtype=torch.int32, device="cuda").expand(len(lens), hk, 8).contiguous()
+    want, want_lse = S.token_attn(q, k, v, kl, idx, cnt)
+    q[:, 2::group] = float("nan")
+    q[:, 1::group, 5] = float("inf")
+    o, lse = S.token_attn(q, k, v, kl, idx, cnt)
+    means = S.block_means(k, kl)
+    o2, lse2, _, _ = S.token_forward(q, k, v, kl, means, 8)
+    for got, got_lse in ((o, lse), (o2, lse2)):
+        for i, n in enumerate(lens):
+            for g in range(group):
+                x, y = got[i, g::group], got_lse[i, g::group]
+                if g == 2 and n:
+                    assert x.isnan().all() and y.isnan().all()
+                elif g != 1 or n == 0:
+                    assert torch.equal(x, want[i, g::group]) and torch.equal(y, want_lse[i, g::group])
+    assert S.device_status() == 0
