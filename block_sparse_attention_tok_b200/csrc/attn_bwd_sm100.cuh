@@ -301,7 +301,7 @@ __device__ __forceinline__ void bwd_sum_parts(const float* src, int n, int64_t s
 // dQ items fill the end of the dK/dV ones. Lists of KV blocks differ in length by a factor of ten (every
 // query block keeps the text blocks): one with more entries than an SM's share of all is split into parts
 // that go first, each storing its fp32 sums; the warp that stores a row range last adds the parts up in
-// order (4 heads, 4,133 queries in 64-token blocks: 70 us, 80 us without; 1 head, 8,192 queries: 87 us,
+// order (4 heads, 4,133 queries in 64-token blocks: 67 us, 82 us without; 1 head, 8,192 queries: 65 us,
 // 112 us). The load thread takes the items and hands them to the other warps through two slots.
 //
 // dK, dV. Tensor memory: S^T [0,128), dP^T [128,256), dV [256,256+D), dK [384,384+D): rows are KV
