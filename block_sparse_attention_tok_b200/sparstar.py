@@ -680,6 +680,28 @@ def _check_token_out(o, lse, q):
         raise ValueError("lse must be contiguous fp32 [B, Hq]")
 
 
+class TokenWorkspace:
+    """Reusable room of token_forward for one shape: the kept lists, through which the CTAs of a
+    launch pass the choice on. The idx and cnt that a call with it returns lie in it until the next
+    such call. Calls that may overlap on the GPU need one each."""
+
+    def __init__(self, n_seq, heads_q, heads_k, capacity, head_dim, keep, device):
+        self.shape = tuple(int(x) for x in (n_seq, heads_q, heads_k, capacity, head_dim, keep))
+        n_seq, heads_q, heads_k, capacity, head_dim, keep = self.shape
+        if n_seq < 0 or min(self.shape[1:]) < 1:
+            raise ValueError(f"no call has {n_seq} sequences, {heads_q} and {heads_k} heads, {capacity} tokens, "
+                             f"head_dim {head_dim} and {keep} blocks")
+        self.buf = torch.empty(n_seq * heads_k * (keep + 1), dtype=torch.int32, device=device)
+        at = n_seq * heads_k * keep
+        self.idx, self.cnt = self.buf[:at].view(n_seq, heads_k, keep), self.buf[at:].view(n_seq, heads_k)
+
+    def check(self, *shape):
+        """Refuses a call of another shape."""
+        if shape != self.shape:
+            raise ValueError(f"the workspace is for (sequences, query heads, key heads, capacity, head_dim, keep) = "
+                             f"{self.shape}, the call has {shape}")
+
+
 def block_means(k: torch.Tensor, kv_len: torch.Tensor, means: Optional[torch.Tensor] = None, tail_only: bool = False,
                 stream=None) -> torch.Tensor:
     """Means of the 128-token blocks of a cache k [B, Hk, S, d] of which sequence b holds kv_len[b]
@@ -745,10 +767,16 @@ def token_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.
 def token_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, means: torch.Tensor,
                   keep: int, n_sink: int = 1, n_recent: int = 1, sm_scale: float = 0.0,
                   o: Optional[torch.Tensor] = None, want_lse: bool = True, lse: Optional[torch.Tensor] = None,
-                  idx: Optional[torch.Tensor] = None, cnt: Optional[torch.Tensor] = None, stream=None):
-    """token_select and token_attn over its choice, in one launch. Returns (o, lse, idx, cnt)."""
+                  idx: Optional[torch.Tensor] = None, cnt: Optional[torch.Tensor] = None, stream=None,
+                  workspace: Optional[TokenWorkspace] = None):
+    """token_select and token_attn over its choice, in one launch. The lists go to idx and cnt where
+    they are given, else to the workspace's, else to new ones. Returns (o, lse, idx, cnt)."""
     b, hk, s, d = _check_cache(k, v, kv_len, means, q)
     keep = int(keep)
+    if workspace is not None:
+        workspace.check(b, q.shape[1], hk, s, d, keep)
+        idx = workspace.idx if idx is None else idx
+        cnt = workspace.cnt if cnt is None else cnt
     _check_lists(idx, cnt, b, hk, keep)
     _check_token_out(o, lse, q)
     _check_device(q.device, idx, cnt, o, lse)
