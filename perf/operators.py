@@ -187,6 +187,9 @@ def prepare(case, seed):
         st["v"] = v
         st["q"] = _randn(gen, b, case["hq"], d).to(BF16)
         st["means"] = _masked_means(st)
+        if own:
+            from block_sparse_attention_tok_b200 import sparstar
+            st["ws"] = sparstar.TokenWorkspace(b, case["hq"], hk, s, d, case["keep"], "cuda")
     return st
 
 
@@ -390,7 +393,7 @@ def run(st):
                                  block=case["block"], workspace=st["ws"])
     if op == "token_forward":
         return sparstar.token_forward(st["q"], st["k"], st["v"], st["lens"], st["means"], case["keep"],
-                                      n_sink=case["sink"], n_recent=case["recent"])
+                                      n_sink=case["sink"], n_recent=case["recent"], workspace=st["ws"])
     return sparstar.block_means(st["k"], st["lens"], st["means"], tail_only=case["tail"])
 
 
