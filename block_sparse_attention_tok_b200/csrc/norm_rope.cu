@@ -312,7 +312,9 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) norm_rope_bwd_kernel(c
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-      const float r = rsqrtf(group_sum<G>(ss) * (1.f / D) + p.eps);
+      // a place without a token or head holds zeros: with eps 0 its root would be infinite, and dw NaN
+      const float mean = group_sum<G>(ss) * (1.f / D);
+      const float r = h < nh ? rsqrtf(mean + p.eps) : 0.f;
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
