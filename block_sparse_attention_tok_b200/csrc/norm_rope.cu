@@ -532,6 +532,7 @@ int sparstar_qk_norm_rope_bwd(sparstar_view dq, sparstar_view dk, sparstar_view 
   int rc = nr_setup({dq_in, dk_in, dv_in}, {dq, dk, dv}, x_dtype, n_tokens, heads_q, heads_k, head_dim, wq, wk, cos,
                     sin, eps, kv_offset, &p);
   if (rc != SPARSTAR_OK) return rc;
+  if (dk.seq_stride != 0 || dv.seq_stride != 0 || q.seq_stride != 0 || k.seq_stride != 0) return SPARSTAR_ERR_ARG;
   const int e = x_dtype == SPARSTAR_BF16 ? 2 : 4;
   if (n_tokens > 0 && (!strides_ok(q, e, n_tokens > 1, heads_q > 1) ||
                        (heads_k > 0 && !strides_ok(k, e, n_tokens > 1, heads_k > 1))))
