@@ -867,11 +867,15 @@ __global__ void __launch_bounds__(BwdConfig<D, B>::kThreads, 1)
 //   past n_q: such a row's P is 0), so that a block's statistics are one aligned copy. One read of
 //   o and do, D / 8 lanes a row; memory-bound.
 //   masks: for each (chunk of 32 query-block rows, head), one word per KV block with the rows that
-//   keep it. A row that lists a block twice is noted in `twice`.
-// bwd_lists_kernel, one CTA per head: the query blocks of each KV block, ascending. Word counts are
-// scanned over chunks and blocks, then every word places its rows. In a chunk with a block listed
-// twice the counts come from the lists themselves (the forward pass attends to it twice, so it is
-// placed twice). Out-of-range entries are clamped as the forward pass clamps them, and recorded.
+//   keep it. A chunk where a row lists a block twice is noted in `twice`, and its words are how often
+//   each block is listed instead (the forward pass attends to it twice, so it counts twice).
+// bwd_lists_kernel, one CTA per head: the query blocks of each KV block, ascending. Counts are
+// scanned over chunks and blocks, then every word places its rows. The rows of a chunk with a block
+// listed twice are placed from their lists, by one warp, row after row, each block's place counting up;
+// which lane takes which of a row's equal entries changes nothing (1 head, 1,000 rows of 200 of 2,000
+// blocks, one of them repeated in every chunk: the call takes 2.06 ms, 1.91 ms where none is; with a search
+// of the chunk's lists for every block 47 ms). Out-of-range entries are clamped as the forward pass clamps
+// them, and recorded.
 constexpr int kMaskRows = 32;
 constexpr int kMaskMaxBlocks = 49152;  // KV blocks at most: one 4-byte word each in shared memory
 
@@ -880,8 +884,8 @@ struct BwdPrep {
   const float* lse;
   const int32_t *idx, *cnt;
   float *neg_lse2, *neg_delta;
-  uint32_t* words;   // [H, chunks, nkb]
-  int32_t* place;    // [H, chunks, nkb] first place of each word's rows within its KV block
+  uint32_t* words;   // [H, chunks, nkb] the rows that keep a block, or (twice) how often it is listed
+  int32_t* place;    // [H, chunks, nkb] place of each word's first (twice: next) row within its KV block
   int32_t* twice;    // [H, chunks]
   int32_t *col_at, *col_row;
   BwdPart* parts;
@@ -916,28 +920,37 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdPrep p) {
     }
     if (threadIdx.x == 0) twice = 0;
     __syncthreads();
-    // four entries in flight per thread
+    // f(row, block) of every entry, four in flight per thread
     const uint32_t kmax = p.kmax, total = rows * kmax;  // at most nqb * kmax: 31 bits
-    for (uint32_t i0 = threadIdx.x; i0 < total; i0 += 4 * 256) {
-      int j[4], r[4];
+    auto entries = [&](auto f) {
+      for (uint32_t i0 = threadIdx.x; i0 < total; i0 += 4 * 256) {
+        int j[4], r[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const uint32_t i = i0 + u * 256;
-        r[u] = i < total ? static_cast<int>(i / kmax) : -1;
-        if (r[u] >= 0 && static_cast<int>(i - r[u] * kmax) < counts[r[u]])
-          j[u] = __ldg(p.idx + row0 * p.kmax + i);
-        else
-          r[u] = -1;
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (r[u] >= 0) {
-          const int jc = bwd_block(j[u], p.nkb);
-          if (jc != j[u]) atomicOr(p.status, kStatusBounds);
-          if ((atomicOr(&words[jc], 1u << r[u]) >> r[u]) & 1u) twice = 1;
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t i = i0 + u * 256;
+          r[u] = i < total ? static_cast<int>(i / kmax) : -1;
+          if (r[u] >= 0 && static_cast<int>(i - r[u] * kmax) < counts[r[u]])
+            j[u] = __ldg(p.idx + row0 * p.kmax + i);
+          else
+            r[u] = -1;
         }
-    }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r[u] >= 0) f(r[u], j[u]);
+      }
+    };
+    entries([&](int r, int j) {
+      const int jc = bwd_block(j, p.nkb);
+      if (jc != j) atomicOr(p.status, kStatusBounds);
+      if ((atomicOr(&words[jc], 1u << r) >> r) & 1u) twice = 1;
+    });
     __syncthreads();
+    if (twice) {
+      for (int j = threadIdx.x; j < p.nkb; j += 256) words[j] = 0u;
+      __syncthreads();
+      entries([&](int, int j) { atomicAdd(&words[bwd_block(j, p.nkb)], 1u); });
+      __syncthreads();
+    }
     uint32_t* out = p.words + static_cast<int64_t>(blockIdx.x) * p.nkb;
     for (int j = threadIdx.x; j < p.nkb; j += 256) out[j] = words[j];
     if (threadIdx.x == 0) p.twice[blockIdx.x] = twice;
@@ -970,22 +983,6 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const BwdPrep p) {
   }
 }
 
-// How often the rows of a chunk list block j; with `out` each listing's row is written there.
-__device__ inline int bwd_scan_lists(const BwdPrep& p, int h, int chunk, int j, int32_t* out) {
-  const int r1 = min(p.nqb, (chunk + 1) * kMaskRows);
-  int n = 0;
-  for (int i = chunk * kMaskRows; i < r1; ++i) {
-    const int64_t row = static_cast<int64_t>(h) * p.nqb + i;
-    const int c = bwd_count(__ldg(p.cnt + row), p.kmax);
-    for (int e = 0; e < c; ++e)
-      if (bwd_block(__ldg(p.idx + row * p.kmax + e), p.nkb) == j) {
-        if (out != nullptr) out[n] = i;
-        ++n;
-      }
-  }
-  return n;
-}
-
 __global__ void __launch_bounds__(1024) bwd_lists_kernel(const BwdPrep p) {
   __shared__ int32_t warp_sum[32];
   __shared__ int32_t base;
@@ -1010,7 +1007,7 @@ __global__ void __launch_bounds__(1024) bwd_lists_kernel(const BwdPrep p) {
         for (int u = 0; u < 8; ++u)
           if (c0 + u < p.n_chunks) {
             place[static_cast<int64_t>(c0 + u) * p.nkb + j] = total;
-            total += twice[c0 + u] ? bwd_scan_lists(p, h, c0 + u, j, nullptr) : __popc(x[u]);
+            total += twice[c0 + u] ? static_cast<int>(x[u]) : __popc(x[u]);
           }
       }
     int incl = total;
@@ -1053,12 +1050,24 @@ __global__ void __launch_bounds__(1024) bwd_lists_kernel(const BwdPrep p) {
   const int64_t n_words = static_cast<int64_t>(p.n_chunks) * p.nkb;
   for (int64_t i = threadIdx.x; i < n_words; i += 1024) {
     const int chunk = static_cast<int>(i / p.nkb), j = static_cast<int>(i - static_cast<int64_t>(chunk) * p.nkb);
+    if (twice[chunk]) continue;
     uint32_t word = words[i];
     int32_t* out = rows + at[j] + place[i];
-    if (twice[chunk]) {
-      if (word != 0u) bwd_scan_lists(p, h, chunk, j, out);
-    } else {
-      for (; word != 0u; word &= word - 1u) *out++ = chunk * kMaskRows + __ffs(word) - 1;
+    for (; word != 0u; word &= word - 1u) *out++ = chunk * kMaskRows + __ffs(word) - 1;
+  }
+  for (int chunk = w; chunk < p.n_chunks; chunk += 32) {
+    if (!twice[chunk]) continue;
+    const int r1 = min(p.nqb, (chunk + 1) * kMaskRows);
+    int32_t* next = place + static_cast<int64_t>(chunk) * p.nkb;
+    for (int i = chunk * kMaskRows; i < r1; ++i) {
+      const int64_t row = static_cast<int64_t>(h) * p.nqb + i;
+      const int c = bwd_count(__ldg(p.cnt + row), p.kmax);
+#pragma unroll 4
+      for (int e = lane; e < c; e += 32) {
+        const int j = bwd_block(__ldg(p.idx + row * p.kmax + e), p.nkb);
+        rows[at[j] + atomicAdd(next + j, 1)] = i;
+      }
+      __syncwarp();  // the next row's places come behind this one's
     }
   }
 }
