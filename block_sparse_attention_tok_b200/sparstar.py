@@ -719,15 +719,19 @@ def block_means(k: torch.Tensor, kv_len: torch.Tensor, means: Optional[torch.Ten
 
 def token_select(q: torch.Tensor, means: torch.Tensor, kv_len: torch.Tensor, keep: int, n_sink: int = 1,
                  n_recent: int = 1, idx: Optional[torch.Tensor] = None, cnt: Optional[torch.Tensor] = None,
-                 stream=None):
+                 stream=None, capacity: Optional[int] = None):
     """Blocks that one query token per sequence, q [B, Hq, d], keeps: per (sequence, key head) the
     first n_sink, the last n_recent and the best others by the query heads' score against the
-    block means, `keep` in all (every block where a sequence has no more). Returns (idx int32
+    block means, `keep` in all (every block where a sequence has no more). capacity is the cache's S,
+    beyond which a length is clamped and reported (default: whole blocks). Returns (idx int32
     [B, Hk, keep], ascending, -1 behind the last, and cnt int32 [B, Hk])."""
     if means.dim() != 4:
         raise ValueError("means must be contiguous fp32 [B, Hk, blocks, d]")
     b, hk, nb, d = means.shape
     keep = int(keep)
+    capacity = nb * BLOCK if capacity is None else int(capacity)
+    if -(-capacity // BLOCK) != nb:
+        raise ValueError(f"a capacity of {capacity} tokens does not have {nb} blocks")
     _check_means(means, b, hk, nb, d)
     _check_kv_len(kv_len, b)
     _check_token_q(q, b, hk, d)
@@ -736,7 +740,7 @@ def token_select(q: torch.Tensor, means: torch.Tensor, kv_len: torch.Tensor, kee
     with _launch(q.device, stream) as st:
         idx = q.new_empty((b, hk, max(keep, 0)), dtype=torch.int32) if idx is None else idx
         cnt = q.new_empty((b, hk), dtype=torch.int32) if cnt is None else cnt
-        _check(load().sparstar_token_select(_at(q), _at(means), _at(kv_len), b, q.shape[1], hk, nb * BLOCK, d, keep,
+        _check(load().sparstar_token_select(_at(q), _at(means), _at(kv_len), b, q.shape[1], hk, capacity, d, keep,
                                             int(n_sink), int(n_recent), _at(idx), _at(cnt), st),
                "sparstar_token_select")
     return idx, cnt
