@@ -45,7 +45,8 @@ int set_kernel_attrs(const DeviceInfo* dev) {
 // Entries of a part of a list: an SM's share of all entries, so that no list holds a CTA longer than the
 // others work, but enough tiles to be worth the sums that a part stores (16 at least; with 8, 12 or 24 the
 // 8 heads of 4,096 queries take the same 74 to 76 us). A list of n > part entries makes
-// ceil(n / part) < 2 n / part parts: with entries / 148 <= part, below 296 in all.
+// ceil(n / part) < 2 n / part parts: with entries / 148 <= part, below 296 in all. 148: a B200's SMs, a
+// constant because a workspace's size is asked for without a device.
 int64_t bwd_part_entries(int heads, int64_t nqb, int32_t kmax) {
   const int64_t share = (static_cast<int64_t>(heads) * nqb * kmax + 147) / 148;
   return share < 16 ? 16 : share;

@@ -11,7 +11,8 @@
 // and walks its KV blocks (3 products a tile). That is 7 products where 5 would do, but every
 // output element has one writer and a fixed order of additions, so the same inputs give the
 // same bits, as in the forward pass; the one-pass form would also add 64 KB of fp32 reductions
-// a tile (about twice what the tile reads) and has no room for them in tensor memory.
+// a tile, as much as a dK/dV tile reads of Q and dO, and its fifth product would have to take turns
+// with S: S, dP, dV and dK fill tensor memory. A form that stores dS for the dQ items has not been built.
 //
 // One persistent kernel does both, one CTA per SM: 8 softmax warps (two per TMEM lane quarter,
 // each pair splitting the 128 columns of a tile), a TMA warp, an MMA warp. A thread keeps half a

@@ -14,9 +14,9 @@
 //
 // Bound: memory. Each value is read once and written once, nothing is staged: d/8 neighbouring
 // lanes hold one head vector (8 values each, so that both members of every pair are in one
-// lane: no exchange but the sum of squares), and an item is one token x up to kHeads heads of
-// one kind, loaded together before any is used (kHeads x 16 bytes in flight per lane), which
-// also reads the token's angles once per item.
+// lane: no exchange but the sum of squares), and an item is one token x up to H heads of
+// one kind (1, 2 or 4 by the call's size), loaded together before any is used (H x 16 bytes in flight
+// per lane in bf16, H x 32 in fp32), which also reads the token's angles once per item.
 #include <cuda_bf16.h>
 
 #include <cmath>

@@ -50,8 +50,9 @@ extern "C" {
 
 #define SPARSTAR_BLOCK 128
 /* 2: adds sparstar_map_scores and sparstar_read_probe (every version-1 entry point unchanged).
- * It counts changes of entry points, not additions: sparstar_qk_norm_rope, sparstar_attn_bwd,
- * sparstar_token_* and sparstar_block_means came later under the same number. */
+ * Additions since then have not raised it: whether a library has sparstar_qk_norm_rope,
+ * sparstar_attn_bwd, sparstar_token_* and sparstar_block_means (and their kin) shows by looking the
+ * symbol up, not by this number. */
 #define SPARSTAR_ABI_VERSION 2
 
 /* Return codes. */
