@@ -9,6 +9,7 @@ import pytest
 import torch
 
 from tests import token_ref as R
+from tests.conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 
@@ -86,5 +87,6 @@ assert all(torch.equal(a, b) for a, b in zip(got, want) if a is not None)
 
 @pytest.mark.parametrize("which", ["norm", "gradient", "token"])
 def test_the_first_call_of_a_process_may_be_captured(S, which):
-    run = subprocess.run([sys.executable, "-c", FIRST.format(which=which)], capture_output=True, text=True, timeout=300)
+    run = subprocess.run([sys.executable, "-c", FIRST.format(which=which)], capture_output=True, text=True, timeout=300,
+                         cwd=ROOT)
     assert run.returncode == 0, run.stderr[-2000:]
